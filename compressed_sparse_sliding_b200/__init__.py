@@ -18,6 +18,8 @@ Entry points (same names as the C ABI):
                        indexer, attention and decode append over them
   hyb_attn_bwd,        gradients for training: through the attention (fixed
   hyb_hca_compress_bwd selection) and through block_merge
+  hyb_prefix_attn_fwd  attention for a batch whose sequences share a prefix of
+                       compressed entries, stored and read once
   hyb_workspace_size, hyb_get_device_status, hyb_error_string
 """
 from __future__ import annotations
@@ -96,6 +98,10 @@ try:
     _lib.hyb_hca_compress_bwd_workspace_size.restype = ctypes.c_size_t
     _lib.hyb_hca_compress_bwd.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
     _lib.hyb_hca_compress_bwd.restype = _I
+    _lib.hyb_prefix_workspace_size.argtypes = [_PP, _I]
+    _lib.hyb_prefix_workspace_size.restype = ctypes.c_size_t
+    _lib.hyb_prefix_attn_fwd.argtypes = [_PP, _I] + [_P] * 10 + [ctypes.c_size_t, _P]
+    _lib.hyb_prefix_attn_fwd.restype = _I
     _lib.hyb_get_device_status.argtypes = [_P]
     _lib.hyb_get_device_status.restype = _I
     _lib.hyb_error_string.argtypes = [_I]
@@ -377,6 +383,88 @@ def hyb_gated_fwd(p: HybProblem, q, kc, vc, idx, k_raw, v_raw, gate, o=None, ws=
     st = _lib.hyb_gated_fwd(ctypes.byref(p), _ptr(q), _ptr(kc), _ptr(vc), _ptr(idx), _ptr(k_raw),
                             _ptr(v_raw), _ptr(gate), _ptr(o), _ptr(ws), ws.numel(), _stream(stream))
     _check(st, "hyb_gated_fwd")
+    return o
+
+
+# ------------------------------------------------- shared and bounded caches
+def _want(name: str, t: Optional[torch.Tensor], shape, dtype, device, needed: bool = True):
+    """ValueError unless t is a contiguous tensor of this shape, type and device
+    (None only where it is not needed)."""
+    if t is None:
+        if needed:
+            raise ValueError(f"{name} is missing")
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         + ("" if t.is_contiguous() else ", not contiguous"))
+
+
+def _want_positions(p: HybProblem, device):
+    q_pos, kv_pos0 = getattr(p, "_keep", (None, None))
+    _want("q_pos", q_pos, (p.B, p.Lq), torch.int32, device, needed=False)
+    _want("kv_pos0", kv_pos0, (p.B,), torch.int32, device, needed=False)
+
+
+class _On:
+    """Makes a tensor's device the current one for a call, and names its stream
+    (the one given, else the device's current stream)."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if t.device.type != "cuda":
+            raise ValueError("the library takes CUDA tensors")
+        self.device = torch.cuda.device(t.device)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(t.device)
+        self.other = stream is not None and stream != torch.cuda.current_stream(t.device)
+
+    def new(self, shape, dtype):
+        """A tensor for this call; the allocator keeps it until the stream is done with it."""
+        t = torch.empty(shape, dtype=dtype, device=self.stream.device)
+        if self.other:
+            t.record_stream(self.stream)
+        return t
+
+    def __enter__(self):
+        self.device.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        self.device.__exit__(*exc)
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+
+def hyb_prefix_workspace_size(p: HybProblem, Np: int) -> int:
+    return int(_lib.hyb_prefix_workspace_size(ctypes.byref(p), int(Np)))
+
+
+def hyb_prefix_attn_fwd(p: HybProblem, q, kp, vp, kc=None, vc=None, k_raw=None, v_raw=None, o=None, lse=None,
+                        ws=None, stream=None):
+    """One softmax over the entries kp / vp [Np, Hkv, d] that every sequence
+    shares, the sequence's own entries kc / vc [B, Nc, Hkv, d] (entry Np + j is
+    row j) and its raw window.  Returns o [B, Lq, Hq, d] bf16; lse [B, Hq, Lq]
+    fp32 is filled when given."""
+    bf, Np = torch.bfloat16, 0 if kp is None else kp.shape[0]
+    _want("q", q, (p.B, p.Lq, p.Hq, p.d), bf, q.device)
+    for name, t, shape, n in (("kp", kp, (Np,), Np), ("vp", vp, (Np,), Np), ("kc", kc, (p.B, p.Nc), p.Nc),
+                              ("vc", vc, (p.B, p.Nc), p.Nc), ("k_raw", k_raw, (p.B, p.Lkv), p.W),
+                              ("v_raw", v_raw, (p.B, p.Lkv), p.W)):
+        _want(name, t, (*shape, p.Hkv, p.d), bf, q.device, needed=n > 0)
+    _want_positions(p, q.device)
+    with _On(q, stream) as on:
+        if o is None:
+            o = on.new((p.B, p.Lq, p.Hq, p.d), bf)
+        _want("o", o, (p.B, p.Lq, p.Hq, p.d), bf, q.device)
+        _want("lse", lse, (p.B, p.Hq, p.Lq), torch.float32, q.device, needed=False)
+        need = hyb_prefix_workspace_size(p, Np)
+        if ws is None or ws.numel() * ws.element_size() < need:
+            ws = on.new((max(need, 256),), torch.uint8)
+        st = _lib.hyb_prefix_attn_fwd(ctypes.byref(p), Np, _ptr(q), _ptr(kp), _ptr(vp), _ptr(kc), _ptr(vc),
+                                      _ptr(k_raw), _ptr(v_raw), _ptr(o), _ptr(lse), _ptr(ws),
+                                      ws.numel() * ws.element_size(), on.handle)
+    _check(st, "hyb_prefix_attn_fwd")
     return o
 
 

@@ -222,6 +222,32 @@ hyb_status hyb_gated_fwd(const hyb_problem *p, const void *q, const void *kc, co
                          const float *gate, void *o, void *ws, size_t ws_bytes,
                          cudaStream_t stream);
 
+/* Attention for a batch that shares a prefix (hyb_attn_fwd with idx == NULL,
+ * for sequences whose first Np compressed entries are the same): entries
+ * 0 .. Np-1 of every sequence are the rows of kp / vp, stored once, and entry
+ * Np + j of sequence b is row j of its own cache kc / vc.  One softmax per
+ * (b, t, h) over
+ *   the shared and own entries visible to the query (entry e, over both), and
+ *   raw keys  positions max(0, t-W+1) .. t (rows p - kv_pos0[b]),
+ * with o, lse, an empty key set and positions as in hyb_attn_fwd.  m = 1, W = 0
+ * makes every entry one token: plain attention behind a shared prompt.
+ * The prefix is read once for the query rows of all sequences together, and
+ * long key ranges are split over the GPU and joined from fp32 partial results
+ * in ws (the join is in a fixed order: equal calls give equal bits).
+ * p: topk <= 0 (else HYB_ERR_UNSUPPORTED), scale >= 0; Nc, Np and W may be 0,
+ * and the pointers of absent parts NULL.  q: [B, Lq, Hq, d]; kp, vp:
+ * [Np, Hkv, d]; kc, vc: [B, Nc, Hkv, d]; k_raw, v_raw: [B, Lkv, Hkv, d], all
+ * bf16 and 16-byte aligned; o: [B, Lq, Hq, d] bf16; lse: [B, Hq, Lq] fp32
+ * (nullable).  Entries that no query of the batch (shared) or of the sequence
+ * (own) sees may hold anything, NaN included; so may raw rows outside a
+ * sequence's windows (from its lowest to its highest query position).
+ * ws: hyb_prefix_workspace_size(p, Np) bytes, 256-byte aligned; calls that may
+ * run at the same time need a workspace each. */
+size_t hyb_prefix_workspace_size(const hyb_problem *p, int Np);
+hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, const void *kp, const void *vp,
+                               const void *kc, const void *vc, const void *k_raw, const void *v_raw, void *o,
+                               float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Backward pass for training (Tiny-R2 README, "Training"), with the top-K
  * selection taken as fixed (the pages define no gradient for it).
  * hyb_attn_bwd: gradients of sum(dout * o) through hyb_attn_fwd for the same
