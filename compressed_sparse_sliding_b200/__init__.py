@@ -20,6 +20,9 @@ Entry points (same names as the C ABI):
   hyb_hca_compress_bwd selection) and through block_merge
   hyb_prefix_attn_fwd  attention for a batch whose sequences share a prefix of
                        compressed entries, stored and read once
+  hyb_attn_weights     the attention weight each cached entry received
+  hyb_evict_select,    eviction from full caches by that weight: the entries to
+  hyb_cache_compact*   keep, and the (bf16 or 4-bit) caches rewritten with them
   hyb_workspace_size, hyb_get_device_status, hyb_error_string
 """
 from __future__ import annotations
@@ -102,6 +105,14 @@ try:
     _lib.hyb_prefix_workspace_size.restype = ctypes.c_size_t
     _lib.hyb_prefix_attn_fwd.argtypes = [_PP, _I] + [_P] * 10 + [ctypes.c_size_t, _P]
     _lib.hyb_prefix_attn_fwd.restype = _I
+    _lib.hyb_attn_weights.argtypes = [_PP] + [_P] * 4 + [_I, _P, _I, _P]
+    _lib.hyb_attn_weights.restype = _I
+    _lib.hyb_evict_select.argtypes = [_P, _I, _I, _P, _I, _I, _I, _P, _P]
+    _lib.hyb_evict_select.restype = _I
+    _lib.hyb_cache_compact.argtypes = [_PP, _P, _I, _I] + [_P] * 9
+    _lib.hyb_cache_compact.restype = _I
+    _lib.hyb_cache_compact_fp4.argtypes = [_PP, _P, _I, _I] + [_P] * 15
+    _lib.hyb_cache_compact_fp4.restype = _I
     _lib.hyb_get_device_status.argtypes = [_P]
     _lib.hyb_get_device_status.restype = _I
     _lib.hyb_error_string.argtypes = [_I]
@@ -466,6 +477,110 @@ def hyb_prefix_attn_fwd(p: HybProblem, q, kp, vp, kc=None, vc=None, k_raw=None, 
                                       ws.numel() * ws.element_size(), on.handle)
     _check(st, "hyb_prefix_attn_fwd")
     return o
+
+
+def hyb_attn_weights(p: HybProblem, q, kc, lse, idx=None, acc=None, accumulate: bool = True, e0: int = 0,
+                     stream=None):
+    """The attention weight that each entry of kc [B, Nc, Hkv, d] received,
+    summed over heads and query tokens, from the attention's lse [B, Hq, Lq];
+    over the entries idx [B, 1, topk] lists when given.  Added to acc [B, Nc]
+    fp32 (accumulate=False: written, 0 for unseen entries); a new tensor when
+    acc is None.  e0: entry index of kc's row 0.  Returns acc."""
+    _want("q", q, (p.B, p.Lq, p.Hq, p.d), torch.bfloat16, q.device)
+    _want("kc", kc, (p.B, p.Nc, p.Hkv, p.d), torch.bfloat16, q.device)
+    _want("lse", lse, (p.B, p.Hq, p.Lq), torch.float32, q.device)
+    _want("idx", idx, (p.B, p.Lq, p.topk), torch.int32, q.device, needed=p.topk > 0)
+    _want("acc", acc, (p.B, p.Nc), torch.float32, q.device, needed=False)
+    _want_positions(p, q.device)
+    with _On(q, stream) as on:
+        if acc is None:
+            acc, accumulate = on.new((p.B, p.Nc), torch.float32), False
+        st = _lib.hyb_attn_weights(ctypes.byref(p), _ptr(q), _ptr(kc), _ptr(lse), _ptr(idx), int(e0), _ptr(acc),
+                                   int(bool(accumulate)), on.handle)
+    _check(st, "hyb_attn_weights")
+    return acc
+
+
+def hyb_evict_select(acc, n_keep: int, n_first: int = 0, n_last: int = 0, n_valid=None, keep=None, stream=None):
+    """The entries each sequence keeps, [B, n_keep] int32 ascending, -1 padded:
+    the first n_first, the last n_last and the heaviest of the rest by
+    acc [B, Nc] fp32, of the n_valid [B] int32 entries it holds (None: all)."""
+    B, Nc = acc.shape
+    _want("acc", acc, (B, Nc), torch.float32, acc.device)
+    _want("n_valid", n_valid, (B,), torch.int32, acc.device, needed=False)
+    with _On(acc, stream) as on:
+        if keep is None:
+            keep = on.new((B, n_keep), torch.int32)
+        _want("keep", keep, (B, n_keep), torch.int32, acc.device)
+        st = _lib.hyb_evict_select(_ptr(acc), B, Nc, _ptr(n_valid), int(n_keep), int(n_first), int(n_last),
+                                   _ptr(keep), on.handle)
+    _check(st, "hyb_evict_select")
+    return keep
+
+
+def _compact_pairs(p, keep, No, on, parts):
+    """(source, output) of every tensor of a compaction; parts: (name, source,
+    output, row shape, dtype), outputs allocated when absent."""
+    out = []
+    for name, x, y, row, dtype in parts:
+        _want(name, x, (p.B, p.Nc, *row), dtype, keep.device, needed=False)
+        if x is not None and y is None:
+            y = on.new((p.B, No, *row), dtype)
+        if x is None and y is not None:
+            raise ValueError(f"{name}_out given without {name}")
+        _want(name + "_out", y, (p.B, No, *row), dtype, keep.device, needed=False)
+        out.append((x, y))
+    return out
+
+
+def _compact_rows(p, keep, outs):
+    """Rows per sequence of the outputs: those of the tensors given, else n_keep."""
+    if keep.dim() != 2:
+        raise ValueError("keep: expected [B, n_keep]")
+    _want("keep", keep, (p.B, keep.shape[1]), torch.int32, keep.device)
+    return next((y.shape[1] for y in outs if y is not None), keep.shape[1])
+
+
+def hyb_cache_compact(p: HybProblem, keep, kc=None, vc=None, kic=None, acc=None, kc_out=None, vc_out=None,
+                      kic_out=None, acc_out=None, stream=None):
+    """Rewrites caches with the entries of keep [B, n_keep] (hyb_evict_select):
+    kc / vc [B, Nc, Hkv, d], kic [B, Nc, di] bf16, acc [B, Nc] fp32, each
+    optional, into outputs of No >= n_keep rows per sequence (new tensors of
+    n_keep rows when absent; their rows without an entry are not initialised).
+    Returns dict(kc, vc, kic, acc) of the outputs."""
+    bf = torch.bfloat16
+    No = _compact_rows(p, keep, (kc_out, vc_out, kic_out, acc_out))
+    with _On(keep, stream) as on:
+        pairs = _compact_pairs(p, keep, No, on, (
+            ("kc", kc, kc_out, (p.Hkv, p.d), bf), ("vc", vc, vc_out, (p.Hkv, p.d), bf),
+            ("kic", kic, kic_out, (p.di,), bf), ("acc", acc, acc_out, (), torch.float32)))
+        st = _lib.hyb_cache_compact(ctypes.byref(p), _ptr(keep), keep.shape[1], No, *(_ptr(x) for x, _ in pairs),
+                                    *(_ptr(y) for _, y in pairs), on.handle)
+    _check(st, "hyb_cache_compact")
+    return dict(zip(("kc", "vc", "kic", "acc"), (y for _, y in pairs)))
+
+
+def hyb_cache_compact_fp4(p: HybProblem, keep, kc: Optional[Fp4Cache] = None, vc: Optional[Fp4Cache] = None,
+                          kic: Optional[Fp4Cache] = None, acc=None, kc_out: Optional[Fp4Cache] = None,
+                          vc_out: Optional[Fp4Cache] = None, kic_out: Optional[Fp4Cache] = None, acc_out=None,
+                          stream=None):
+    """hyb_cache_compact over 4-bit caches."""
+    both = lambda c: (None, None) if c is None else (c.codes, c.qp)
+    No = _compact_rows(p, keep, (*both(kc_out), *both(vc_out), *both(kic_out), acc_out))
+    with _On(keep, stream) as on:
+        parts = []
+        for name, c, o, row, dx in (("kc", kc, kc_out, (p.Hkv,), p.d), ("vc", vc, vc_out, (p.Hkv,), p.d),
+                                    ("kic", kic, kic_out, (), p.di)):
+            (x, xq), (y, yq) = both(c), both(o)
+            parts += [(name, x, y, (*row, dx // 2), torch.uint8), (name + " pairs", xq, yq, (*row, 2), torch.float32)]
+        pairs = _compact_pairs(p, keep, No, on, (*parts, ("acc", acc, acc_out, (), torch.float32)))
+        st = _lib.hyb_cache_compact_fp4(ctypes.byref(p), _ptr(keep), keep.shape[1], No,
+                                        *(_ptr(x) for x, _ in pairs), *(_ptr(y) for _, y in pairs), on.handle)
+    _check(st, "hyb_cache_compact_fp4")
+    out = [y for _, y in pairs]
+    got = {n: None if out[2 * i] is None else Fp4Cache(out[2 * i], out[2 * i + 1])
+           for i, n in enumerate(("kc", "vc", "kic"))}
+    return dict(got, acc=out[6])
 
 
 def hyb_get_device_status(stream=None) -> int:

@@ -1,0 +1,518 @@
+// attn_weights.cu -- the attention weight that each cached entry received:
+//   acc[b, j] (+)= sum over query tokens t and heads h of
+//                  exp(scale q[b, t, h] . kc[b, j, h / g] - lse[b, h, t])
+// over the entries j that are visible to t (or that idx lists), with the lse of
+// the attention that ran before.  What an eviction keeps a cache by.
+//
+// Mathematics and bound.  lse is known, so the softmax needs no running
+// maximum: each score is exponentiated once and summed over the query rows.
+// K is read once (2 d bytes per entry and KV head) and nothing of size
+// rows x entries is ever stored; with few query rows (decode) the K stream from
+// HBM bounds it, with many (the last tokens of a prompt) the exponentials.
+//
+// Layout.  S^T = K Q^T on tcgen05: keys are the MMA's M, so a TMEM lane is a key
+// and the sum over query rows stays inside one thread (no reduction across
+// threads, no atomics between CTAs: each entry has one owner, and equal calls
+// give equal bits).  A CTA owns a run of key-tile pairs of one or more sequences;
+// two epilogue warpgroups take one tile of the pair each, from two S buffers a
+// tile (4 x 128 TMEM columns), so the MMA of the next query block runs under
+// the exponentials of this one.  Query blocks (hpt heads x tpt tokens, up to
+// 128 rows) stay in shared memory for the whole run where all of a sequence's
+// fit 64 KB (decode), and stream through the same slots otherwise.
+//
+// Roles (512 threads): warps 0-3 / 4-7 epilogue of tile A / B (thread = key),
+// warp 8 TMA producer, warp 9 MMA issue, warp 10 writes each query block's lse
+// and visible counts beside it, warps 12-15 gather the selected rows with
+// cp.async when idx is given (16 lanes per row).
+#include "common.cuh"
+
+namespace hyb {
+
+constexpr int kAwThreads = 512;
+constexpr int kAwBM = 128;          // keys of a tile
+constexpr int kAwKStages = 4;
+constexpr int kAwQBytes = 64 * 1024;
+constexpr int kAwQStages = 16;      // barrier slots; the bytes usually bind first
+
+struct WeightParams {
+    int B, Lq, Hq, Hkv, g, Nc, m, W, e0, K;
+    int hpt, tpt, nht, nblk;        // heads and tokens of a query block, head tiles, blocks per KV head
+    int NB;                         // MMA columns of a block (rows rounded up to 16)
+    int nqs, resident;              // query slots; all blocks of a sequence fit them
+    int pairs;                      // key-tile pairs of a full cache (idx: of the selection)
+    long long total;                // B * pairs
+    int accumulate;
+    float scale_log2;
+    const int32_t *q_pos, *idx;
+    const float *lse;
+    const __nv_bfloat16 *kc;
+    float *acc;
+};
+
+template <int D>
+struct WeightSmem {
+    static constexpr int K_BYTES = kAwBM * D * 2;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = kAwQBytes;
+    static constexpr int OFF_COL = OFF_K + kAwKStages * K_BYTES;     // -lse (log2) per column, then counts
+    static constexpr int NCOL = kAwQBytes / (D * 2);                 // columns of all slots together
+    static constexpr int OFF_BAR = OFF_COL + NCOL * 8;
+    static constexpr int OFF_MISC = OFF_BAR + 64 * 8;
+    static constexpr int BYTES = OFF_MISC + 128;
+};
+
+// barrier slots
+enum { WB_QF = 0, WB_QE = 16, WB_KF = 32, WB_KE = 36, WB_SF = 40, WB_SE = 44, WB_DONE = 48 };
+
+// A stretch of one sequence's key-tile pairs, the work of a CTA between two
+// sequence changes.
+struct WeightRun {
+    int b, nv;         // sequence; entries that some query token of it sees
+    int ntiles;        // key tiles (idx: of the selection)
+    int lo, hi;        // pairs of this run
+    int z0, z1;        // entries this run zeroes (those no query token sees)
+};
+
+__device__ __forceinline__ int aw_visible(const WeightParams &p, int flat)
+{
+    const long long pos = p.q_pos ? p.q_pos[flat] : flat % p.Lq;
+    const int nv = pf_visible(pos, p.m, p.W, p.e0 + p.Nc);
+    return max(nv - p.e0, 0);
+}
+
+// The run that starts at pair u of the CTA's range [u, end) of the stream of all
+// sequences' pairs, which counts full caches: a sequence's pairs that hold
+// visible entries are spread over its share of the range.  Whole warp.
+__device__ __forceinline__ WeightRun weight_run(const WeightParams &p, long long u, long long end, int lane,
+                                                long long &next)
+{
+    WeightRun r;
+    r.b = (int)(u / p.pairs);
+    const int a0 = (int)(u % p.pairs);
+    const int a1 = (int)min((long long)p.pairs, a0 + (end - u));
+    next = u + (a1 - a0);
+    int nv = 0;
+    for (int t = lane; t < p.Lq; t += 32)
+        nv = max(nv, aw_visible(p, r.b * p.Lq + t));
+    r.nv = __reduce_max_sync(0xffffffffu, nv);
+    r.ntiles = ((p.idx ? p.K : r.nv) + kAwBM - 1) / kAwBM;
+    const long long T = (r.ntiles + 1) / 2;
+    r.lo = (int)(T * a0 / p.pairs);
+    r.hi = (int)(T * a1 / p.pairs);
+    r.z0 = r.z1 = 0;
+    if (!p.accumulate && !p.idx) {
+        r.z0 = r.nv + (int)((long long)(p.Nc - r.nv) * a0 / p.pairs);
+        r.z1 = r.nv + (int)((long long)(p.Nc - r.nv) * a1 / p.pairs);
+    }
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAwThreads, 1)
+attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const WeightParams p)
+{
+    pdl_wait();      // launched as a programmatic dependent: the previous kernel's writes
+    pdl_trigger();   // are visible from here on; the next kernel may start its launch
+    using SM = WeightSmem<D>;
+    constexpr int NCB = D / 64;
+    extern __shared__ __align__(1024) uint8_t aw_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(aw_smem_raw) + 1023) &
+                                                ~(uintptr_t)1023);
+    uint8_t *sQ = smem + SM::OFF_Q;
+    uint8_t *sK = smem + SM::OFF_K;
+    float *sLse = reinterpret_cast<float *>(smem + SM::OFF_COL);       // -lse, log2 units, per slot and column
+    int *sNv = reinterpret_cast<int *>(smem + SM::OFF_COL + SM::NCOL * 4);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + SM::OFF_BAR);
+    int *misc = reinterpret_cast<int *>(smem + SM::OFF_MISC);
+    int *sMin = misc + 8;                                              // [16] least count of a slot's columns
+    volatile int *abort_flag = misc + 1;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kAwQStages; ++s) {
+            mbar_init(&bar[WB_QF + s], 1 + 32);    // the TMA copy, warp 10's lanes
+            mbar_init(&bar[WB_QE + s], 1 + 8);     // the MMA, the epilogue warps
+        }
+        for (int s = 0; s < kAwKStages; ++s) {
+            mbar_init(&bar[WB_KF + s], p.idx ? 128 : 1);
+            mbar_init(&bar[WB_KE + s], 1);
+            mbar_init(&bar[WB_SF + s], 1);
+            mbar_init(&bar[WB_SE + s], 128);
+        }
+        mbar_init(&bar[WB_DONE], 1);
+        mbar_fence_init();
+        misc[1] = 0;
+    }
+    if (warp == 9)
+        tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)misc[0];
+
+    const long long u0 = p.total * blockIdx.x / gridDim.x, u1 = p.total * (blockIdx.x + 1) / gridDim.x;
+    const uint32_t qbytes = (uint32_t)p.NB * D * 2;
+    const int nblocks = p.Hkv * p.nblk;            // query blocks of a sequence
+    // Query slot and fill count of the n-th block use: with resident blocks a
+    // slot is filled once a run, otherwise the blocks go round the slots.
+    auto wait = [&](int b, uint32_t parity) {      // whole warp
+        return __all_sync(0xffffffffu, mbar_wait(&bar[b], parity, abort_flag)) != 0;
+    };
+
+    if (warp == 8 || warp == 10) {
+        // ============ query blocks: copies (warp 8), lse and counts (warp 10); K tiles (warp 8) ============
+        uint32_t kc = 0, qc = 0, runs = 0;
+        bool ok = true;
+        const uint32_t box_bytes = (uint32_t)p.hpt * p.tpt * D * 2;
+        for (long long u = u0; ok && u < u1;) {
+            const WeightRun r = weight_run(p, u, u1, lane, u);
+            for (int pr = r.lo; ok && pr < r.hi; ++pr) {
+                for (int i = 0; ok && i < nblocks; ++i) {
+                    const int h = i / p.nblk, blk = i % p.nblk;
+                    if (warp == 8 && blk == 0 && !p.idx) {
+                        for (int tile = 2 * pr; ok && tile < min(2 * pr + 2, r.ntiles); ++tile) {
+                            const uint32_t st = kc % kAwKStages;
+                            if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
+                                break;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&bar[WB_KF + st], SM::K_BYTES);
+                                for (int cb = 0; cb < NCB; ++cb)
+                                    tma_load_4d(sK + st * SM::K_BYTES + cb * kAwBM * 128, &tm_k, &bar[WB_KF + st],
+                                                cb * 64, h, tile * kAwBM, r.b);
+                            }
+                            __syncwarp();
+                            ++kc;
+                        }
+                        if (!ok)
+                            break;
+                    }
+                    if (p.resident && pr > r.lo)
+                        continue;
+                    const uint32_t st = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
+                    if (fill > 0 && !(ok = wait(WB_QE + st, (fill - 1) & 1)))
+                        break;
+                    ++qc;
+                    const int t0 = (blk / p.nht) * p.tpt, h0 = (blk % p.nht) * p.hpt;
+                    if (warp == 8) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&bar[WB_QF + st], box_bytes);
+                            for (int cb = 0; cb < NCB; ++cb)
+                                tma_load_4d(sQ + st * qbytes + cb * p.NB * 128, &tm_q, &bar[WB_QF + st], cb * 64,
+                                            h * p.g + h0, t0, r.b);
+                        }
+                        __syncwarp();
+                    } else {
+                        int least = INT_MAX;
+                        for (int c = lane; c < p.NB; c += 32) {
+                            const int t = t0 + c / p.hpt, hd = h0 + c % p.hpt;
+                            float l = 0.f;
+                            int nv = 0;
+                            if (c < p.hpt * p.tpt && t < p.Lq && hd < p.g) {
+                                l = -1.4426950408889634f *
+                                    p.lse[((size_t)r.b * p.Hq + h * p.g + hd) * p.Lq + t];
+                                nv = aw_visible(p, r.b * p.Lq + t);
+                                least = min(least, nv);
+                            }
+                            sLse[st * p.NB + c] = l;
+                            sNv[st * p.NB + c] = nv;
+                        }
+                        least = __reduce_min_sync(0xffffffffu, least);
+                        if (lane == 0)
+                            sMin[st] = least;
+                        mbar_arrive(&bar[WB_QF + st]);
+                    }
+                }
+            }
+            if (r.hi > r.lo)
+                ++runs;
+        }
+        if (warp == 8 && lane == 0) {
+            // unwinding: wait for the last copies issued into every slot
+            for (uint32_t c = (kc > kAwKStages ? kc - kAwKStages : 0); c < kc; ++c)
+                drain_wait(&bar[WB_KF + c % kAwKStages], (c / kAwKStages) & 1);
+            if (!p.resident) {
+                for (uint32_t c = (qc > (uint32_t)p.nqs ? qc - p.nqs : 0); c < qc; ++c)
+                    drain_wait(&bar[WB_QF + c % p.nqs], (c / p.nqs) & 1);
+            } else {
+                for (uint32_t c = 0; c < qc && c < (uint32_t)nblocks; ++c)
+                    drain_wait(&bar[WB_QF + c], ((qc - 1 - c) / nblocks) & 1);
+            }
+        }
+    } else if (warp >= 12) {
+        // ============================ selected rows: gather ============================
+        if (p.idx) {
+            constexpr int CH = D / 8;              // 16-byte chunks of a row
+            constexpr int RPI = 128 / CH;          // rows a pass
+            const int pt = threadIdx.x - 12 * 32;
+            const int c8 = pt % CH, rsub = pt / CH;
+            const uint32_t dchunk = (c8 >> 3) * kAwBM * 128;
+            uint32_t kc = 0;
+            bool ok = true;
+            for (long long u = u0; ok && u < u1;) {
+                const WeightRun r = weight_run(p, u, u1, lane, u);
+                for (int pr = r.lo; ok && pr < r.hi; ++pr)
+                    for (int h = 0; ok && h < p.Hkv; ++h)
+                        for (int tile = 2 * pr; tile < min(2 * pr + 2, r.ntiles); ++tile) {
+                            int src[kAwBM / RPI];
+#pragma unroll
+                            for (int i = 0; i < kAwBM / RPI; ++i) {
+                                const int slot = tile * kAwBM + i * RPI + rsub;
+                                const int e = slot < p.K ? p.idx[(size_t)r.b * p.K + slot] : -1;
+                                if (e >= p.Nc && c8 == 0 && h == 0)
+                                    set_error(HYB_ERR_DEVICE_BOUNDS);
+                                src[i] = e < r.nv ? e : -1;
+                            }
+                            const uint32_t st = kc % kAwKStages;
+                            if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
+                                break;
+                            const uint32_t dst = smem_u32(sK + st * SM::K_BYTES) + dchunk;
+#pragma unroll
+                            for (int i = 0; i < kAwBM / RPI; ++i)
+                                cp_async_16(dst + sw128_offset(i * RPI + rsub, c8 & 7),
+                                            p.kc + (((size_t)r.b * p.Nc + max(src[i], 0)) * p.Hkv + h) * D + c8 * 8,
+                                            src[i] >= 0 ? 16u : 0u);
+                            cp_async_mbar_arrive(&bar[WB_KF + st]);
+                            mbar_arrive(&bar[WB_KF + st]);
+                            ++kc;
+                        }
+            }
+            cp_async_wait_group<0>();
+        }
+    } else if (warp == 9) {
+        // ================================ MMA issue ================================
+        const uint32_t idesc = idesc_bf16(kAwBM, p.NB, false, false);
+        const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK);
+        uint32_t kc = 0, qc = 0, runs = 0, sc[2] = {0, 0};
+        bool ok = true;
+        for (long long u = u0; ok && u < u1;) {
+            const WeightRun r = weight_run(p, u, u1, lane, u);
+            for (int pr = r.lo; ok && pr < r.hi; ++pr) {
+                const int nt = min(2, r.ntiles - 2 * pr);
+                for (int i = 0; ok && i < nblocks; ++i) {
+                    const int blk = i % p.nblk;
+                    const uint32_t qs = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
+                    if (!(ok = wait(WB_QF + qs, fill & 1)))
+                        break;
+                    ++qc;
+                    for (int x = 0; ok && x < nt; ++x) {
+                        const uint32_t ks = (kc + x) % kAwKStages, buf = sc[x] & 1;
+                        if (blk == 0) {
+                            if (!(ok = wait(WB_KF + ks, ((kc + x) / kAwKStages) & 1)))
+                                break;
+                            if (p.idx)
+                                fence_proxy_async_smem();   // rows written by cp.async, read by the MMA
+                        }
+                        if (sc[x] >= 2 && !(ok = wait(WB_SE + 2 * x + buf, ((sc[x] >> 1) - 1) & 1)))
+                            break;
+                        tc_fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t da = sw128_desc(aK + ks * SM::K_BYTES + (kk >> 2) * kAwBM * 128 +
+                                                                   (kk & 3) * 32,
+                                                               16, 1024);
+                                const uint64_t db = sw128_desc(aQ + qs * qbytes + (kk >> 2) * p.NB * 128 +
+                                                                   (kk & 3) * 32,
+                                                               16, 1024);
+                                mma_bf16_ss(tmem + x * 256 + buf * 128, da, db, idesc, kk > 0 ? 1u : 0u);
+                            }
+                            mma_commit(&bar[WB_SF + 2 * x + buf]);
+                            if (blk == p.nblk - 1)
+                                mma_commit(&bar[WB_KE + ks]);
+                        }
+                        ++sc[x];
+                    }
+                    if (!ok)
+                        break;
+                    if (blk == p.nblk - 1)
+                        kc += nt;
+                    if (lane == 0 && (!p.resident || pr == r.hi - 1))
+                        mma_commit(&bar[WB_QE + qs]);
+                }
+            }
+            if (r.hi > r.lo)
+                ++runs;
+        }
+        if (lane == 0) {
+            mma_commit(&bar[WB_DONE]);
+            drain_wait(&bar[WB_DONE], 0);
+        }
+    } else if (warp < 8) {
+        // ============================ exponentials and sums ============================
+        const int x = warp >> 2;
+        const int quad = warp & 3;
+        const int key = quad * 32 + lane;
+        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + x * 256;
+        const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
+        uint32_t qc = 0, runs = 0, sc = 0;
+        bool ok = true;
+        for (long long u = u0; ok && u < u1;) {
+            const WeightRun r = weight_run(p, u, u1, lane, u);
+            for (int j = r.z0 + (int)threadIdx.x; j < r.z1; j += 256)
+                p.acc[(size_t)r.b * p.Nc + j] = 0.f;
+            for (int pr = r.lo; ok && pr < r.hi; ++pr) {
+                const int tile = 2 * pr + x;
+                const bool active = tile < r.ntiles;
+                const int j = tile * kAwBM + key;        // entry, or slot of the selection
+                float tot = 0.f;
+                for (int i = 0; ok && i < nblocks; ++i) {
+                    const int blk = i % p.nblk;
+                    const uint32_t qs = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
+                    ++qc;
+                    // an idle warpgroup waits too, so that it never releases a slot
+                    // ahead of the others
+                    if (!(ok = wait(WB_QF + qs, fill & 1)))
+                        break;
+                    if (active) {
+                        if (!(ok = wait(WB_SF + 2 * x + (sc & 1), (sc >> 1) & 1)))
+                            break;
+                        tc_fence_after();
+                        // rows of this block: whole tokens, or the heads of a group's last tile
+                        const int t0 = (blk / p.nht) * p.tpt, h0 = (blk % p.nht) * p.hpt;
+                        const int ncv = min(p.hpt, p.g - h0) * min(p.tpt, p.Lq - t0);
+                        const bool full = p.idx || (tile + 1) * kAwBM <= sMin[qs];
+                        const uint32_t tS = tl + (sc & 1) * 128;
+                        const float *nl = sLse + qs * p.NB;
+                        const int *cn = sNv + qs * p.NB;
+#pragma unroll 1
+                        for (int c = 0; c < ncv; c += 32) {
+                            float sv[32];
+                            tmem_ld32(tS + c, sv);
+                            tmem_ld_wait();
+                            if (full && c + 32 <= ncv) {
+                                uint64_t s2[2] = {0ull, 0ull};
+#pragma unroll
+                                for (int q = 0; q < 32; q += 4) {
+                                    const ulonglong2 l2 = *reinterpret_cast<const ulonglong2 *>(nl + c + q);
+                                    float a0, a1, b0, b1;
+                                    f2_split(fma_f2(f2(sv[q], sv[q + 1]), sc2, l2.x), a0, a1);
+                                    f2_split(fma_f2(f2(sv[q + 2], sv[q + 3]), sc2, l2.y), b0, b1);
+                                    s2[0] = add_f2(s2[0], f2(ex2_approx(a0), ex2_approx(a1)));
+                                    s2[1] = add_f2(s2[1], f2(ex2_approx(b0), ex2_approx(b1)));
+                                }
+                                float a0, a1;
+                                f2_split(add_f2(s2[0], s2[1]), a0, a1);
+                                tot += a0 + a1;
+                            } else {
+                                // some columns are padding, or do not see every key of the tile
+                                float s = 0.f;
+#pragma unroll
+                                for (int q = 0; q < 32; ++q) {
+                                    const bool in = c + q < ncv && (p.idx || j < cn[c + q]);
+                                    const float e = ex2_approx(fmaf(sv[q], p.scale_log2, nl[min(c + q, p.NB - 1)]));
+                                    s += in ? e : 0.f;
+                                }
+                                tot += s;
+                            }
+                        }
+                        tc_fence_before();
+                        mbar_arrive(&bar[WB_SE + 2 * x + (sc & 1)]);
+                        ++sc;
+                    }
+                    if (!p.resident || pr == r.hi - 1) {
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&bar[WB_QE + qs]);   // this warp has read the slot's columns
+                    }
+                }
+                if (!ok || !active)
+                    continue;
+                if (p.idx) {
+                    const int e = j < p.K ? p.idx[(size_t)r.b * p.K + j] : -1;
+                    // an entry listed twice counts twice, whichever is added first
+                    if (e >= 0 && e < r.nv)
+                        atomicAdd(&p.acc[(size_t)r.b * p.Nc + e], tot);
+                } else if (j < r.nv) {
+                    float *a = &p.acc[(size_t)r.b * p.Nc + j];
+                    *a = p.accumulate ? *a + tot : tot;
+                }
+            }
+            if (r.hi > r.lo)
+                ++runs;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc((uint32_t)misc[0], 512);
+    }
+}
+
+__global__ void __launch_bounds__(256) attn_weights_zero_kernel(float *acc, long long n)
+{
+    pdl_wait();
+    pdl_trigger();
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
+        acc[i] = 0.f;
+}
+
+template <int D>
+static cudaError_t launch_weights_t(WeightParams &p, const void *q, const void *kc, cudaStream_t stream,
+                                    int num_sms)
+{
+    using SM = WeightSmem<D>;
+    p.nqs = kAwQBytes / (p.NB * D * 2);
+    if (p.nqs > kAwQStages)
+        p.nqs = kAwQStages;
+    p.resident = (long long)p.Hkv * p.nblk <= p.nqs;
+    CUtensorMap mq, mk;
+    if (!make_map(&mq, q, D, p.Hq, p.Lq, p.B, p.hpt, p.tpt) ||
+        !make_map(&mk, kc, D, p.Hkv, p.Nc, p.B, 1, kAwBM))
+        return cudaErrorInvalidValue;
+    const size_t ask = 1024 + SM::BYTES < 120 * 1024 ? 120 * 1024 : 1024 + SM::BYTES;
+    auto kern = attn_weights_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
+    if (e != cudaSuccess)
+        return e;
+    if (p.idx && !p.accumulate) {
+        const long long n = (long long)p.B * p.Nc;
+        const long long blocks = (n + 1023) / 1024;
+        e = launch_pdl(attn_weights_zero_kernel, dim3((unsigned)(blocks < num_sms * 8 ? blocks : num_sms * 8)),
+                       dim3(256), 0, stream, p.acc, n);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const long long grid = p.total < num_sms ? p.total : num_sms;
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(kAwThreads), ask, stream, mq, mk, p);
+}
+
+cudaError_t launch_attn_weights(int B, int Lq, int Hq, int Hkv, int d, int Nc, int m, int W, int e0, int K,
+                                float scale, const int32_t *q_pos, const void *q, const void *kc,
+                                const float *lse, const int32_t *idx, float *acc, int accumulate,
+                                cudaStream_t stream, int num_sms)
+{
+    WeightParams p = {};
+    p.B = B;
+    p.Lq = Lq;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.Nc = Nc;
+    p.m = m;
+    p.W = W;
+    p.e0 = e0;
+    p.K = idx ? K : 0;
+    p.hpt = p.g < 128 ? p.g : 128;
+    p.tpt = 128 / p.hpt < Lq ? 128 / p.hpt : Lq;
+    p.nht = (p.g + p.hpt - 1) / p.hpt;
+    p.nblk = (Lq + p.tpt - 1) / p.tpt * p.nht;
+    p.NB = (p.hpt * p.tpt + 15) / 16 * 16;
+    const int tiles = ((idx ? K : Nc) + kAwBM - 1) / kAwBM;
+    p.pairs = (tiles + 1) / 2;
+    p.total = (long long)B * p.pairs;
+    p.accumulate = accumulate;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.q_pos = q_pos;
+    p.idx = idx;
+    p.lse = lse;
+    p.kc = static_cast<const __nv_bfloat16 *>(kc);
+    p.acc = acc;
+    return d == 128 ? launch_weights_t<128>(p, q, kc, stream, num_sms)
+                    : launch_weights_t<64>(p, q, kc, stream, num_sms);
+}
+
+}  // namespace hyb

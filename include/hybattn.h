@@ -248,6 +248,63 @@ hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, cons
                                const void *kc, const void *vc, const void *k_raw, const void *v_raw, void *o,
                                float *lse, void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/* The attention weight that cached entries received (what an eviction keeps a
+ * cache by; it reads K a second time instead of storing the weights of the
+ * attention pass, which are larger than K for a group of d / 2 heads or more):
+ *   w[b, j] = sum over t, h of exp(scale q[b,t,h] . kc[b, j, h/(Hq/Hkv)] - lse[b,h,t])
+ * over the entries j that query t sees, or, with idx, over those of them that
+ * idx[b, t, :] lists.  Row j of kc is entry e0 + j (e0 = 0, or the Np of
+ * hyb_prefix_attn_fwd), which is what visibility is decided by; lse is the
+ * output of the attention call of the same step (its window keys took their
+ * share of the softmax; they have no row here).
+ *   accumulate != 0: acc[b, j] += w[b, j] for the entries some query of the
+ *     sequence sees (idx: that it lists); the others are left as they were.
+ *   accumulate == 0: acc[b, j] = w[b, j] for every j < Nc (0 where unseen).
+ * fp32 sums in a fixed order.  q: [B, Lq, Hq, d], kc: [B, Nc, Hkv, d] bf16,
+ * 16-byte aligned; lse: [B, Hq, Lq]; idx: [B, Lq, topk] int32 or NULL (then
+ * topk <= 0), with Lq == 1 (else HYB_ERR_UNSUPPORTED; an entry listed twice
+ * counts twice; entries >= Nc are skipped and flagged as
+ * HYB_ERR_DEVICE_BOUNDS); acc: [B, Nc] fp32.  Unseen rows of kc may hold
+ * anything. */
+hyb_status hyb_attn_weights(const hyb_problem *p, const void *q, const void *kc, const float *lse,
+                            const int32_t *idx, int e0, float *acc, int accumulate, cudaStream_t stream);
+
+/* The entries that a full cache keeps.  Sequence b holds n = n_valid[b] entries
+ * (NULL: Nc; values outside 0 .. Nc are clamped and flagged as
+ * HYB_ERR_DEVICE_BOUNDS).  With n <= n_keep all of them are kept; otherwise the
+ * first n_first, the last n_last and of the rest those with the largest
+ * acc[b, j], n_keep in all (equal weights: the lower index; NaN ranks as
+ * -infinity).  keep[b, :]: their indices, ascending, -1 padded.
+ * acc: [B, Nc] fp32; keep: [B, n_keep] int32; n_first + n_last <= n_keep;
+ * B <= 65535.
+ * Positions after an eviction: the caches of a sequence that lost E entries are
+ * those of one that is m * E tokens shorter; take m * E off the positions given
+ * to later calls (t_new, q_pos).  hyb_decode_append finds its ring rows by
+ * position mod W, so choose n_keep such that m * E is a multiple of W, and
+ * n_last >= ceil(W / m) + 1, so that the entries that still overlap the window
+ * stay the last ones. */
+hyb_status hyb_evict_select(const float *acc, int B, int Nc, const int32_t *n_valid, int n_keep, int n_first,
+                            int n_last, int32_t *keep, cudaStream_t stream);
+
+/* The caches with the kept entries: row i of sequence b of every output becomes
+ * row keep[b, i] of its input (rows whose keep is negative, and rows >= n_keep,
+ * are left as they were; keep >= Nc is skipped and flagged as
+ * HYB_ERR_DEVICE_BOUNDS).  Inputs have p->Nc rows per sequence, outputs
+ * No >= n_keep.  kc, vc: [B, Nc, Hkv, d] -> [B, No, Hkv, d] bf16; kic:
+ * [B, Nc, di] bf16; acc: [B, Nc] fp32; any of them NULL with its output.  No
+ * output may overlap an input or another output (HYB_ERR_INVALID_ARG): with
+ * equal capacities two sets of caches alternate.  p: B, Nc, Hkv, d, di. */
+hyb_status hyb_cache_compact(const hyb_problem *p, const int32_t *keep, int n_keep, int No, const void *kc,
+                             const void *vc, const void *kic, const float *acc, void *kc_out, void *vc_out,
+                             void *kic_out, float *acc_out, cudaStream_t stream);
+/* The same for 4-bit caches (codes and (min, scale) pairs of hyb_fp4_quantize). */
+hyb_status hyb_cache_compact_fp4(const hyb_problem *p, const int32_t *keep, int n_keep, int No,
+                                 const uint8_t *kc_codes, const float *kc_qp, const uint8_t *vc_codes,
+                                 const float *vc_qp, const uint8_t *kic_codes, const float *kic_qp,
+                                 const float *acc, uint8_t *kc_codes_out, float *kc_qp_out,
+                                 uint8_t *vc_codes_out, float *vc_qp_out, uint8_t *kic_codes_out,
+                                 float *kic_qp_out, float *acc_out, cudaStream_t stream);
+
 /* Backward pass for training (Tiny-R2 README, "Training"), with the top-K
  * selection taken as fixed (the pages define no gradient for it).
  * hyb_attn_bwd: gradients of sum(dout * o) through hyb_attn_fwd for the same

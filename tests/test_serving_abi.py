@@ -71,3 +71,99 @@ def test_python_calls_check_shapes_and_types(hb):
             hb.hyb_prefix_attn_fwd(p, **x)
     with pytest.raises(ValueError, match="CUDA"):
         hb.hyb_prefix_attn_fwd(p, q, kp, kp, kc, kc)
+
+
+def _weights(hb, e0=0, swap=None, idx=False, **kw):
+    args = dict(B=2, Lq=1, Lkv=0, Hq=4, Hkv=2, d=64, m=4, W=8, Nc=4, topk=3 if idx else 0)
+    args.update(kw)
+    p = hb.problem(**args)
+    names = ["q", "kc", "lse", "idx", "acc"]
+    ptr = {n: ctypes.c_void_p(4096) for n in names}
+    if not idx:
+        ptr["idx"] = None
+    if swap:
+        ptr[swap[0]] = None if swap[1] is None else ctypes.c_void_p(swap[1])
+    return hb._lib.hyb_attn_weights(ctypes.byref(p), ptr["q"], ptr["kc"], ptr["lse"], ptr["idx"], e0, ptr["acc"], 1,
+                                    None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(e0=-1), "INVALID_ARG"), (dict(scale=-1.0), "INVALID_ARG"), (dict(Nc=0), "INVALID_ARG"),
+    (dict(Hkv=3), "INVALID_ARG"), (dict(topk=3), "INVALID_ARG"), (dict(idx=True, topk=0), "INVALID_ARG"),
+    (dict(swap=("q", None)), "INVALID_ARG"), (dict(swap=("kc", None)), "INVALID_ARG"),
+    (dict(swap=("lse", None)), "INVALID_ARG"), (dict(swap=("acc", None)), "INVALID_ARG"),
+    (dict(swap=("q", 4096 + 8)), "INVALID_ARG"), (dict(swap=("kc", 4096 + 2)), "INVALID_ARG"),
+    (dict(idx=True, Lq=2), "UNSUPPORTED"), (dict(idx=True, topk=2049), "UNSUPPORTED"), (dict(d=32), "UNSUPPORTED"),
+    (dict(e0=1 << 30), "UNSUPPORTED"), (dict(B=1 << 20, Lq=1 << 12), "UNSUPPORTED"),
+])
+def test_weights_refusals(hb, change, status):
+    assert _weights(hb, **change) == getattr(hb, "HYB_ERR_" + status)
+
+
+@pytest.mark.parametrize("args,status", [
+    ((None, 1, 8, 4, 0, 0, True), "INVALID_ARG"), ((True, 1, 8, 4, 0, 0, None), "INVALID_ARG"),
+    ((True, 0, 8, 4, 0, 0, True), "INVALID_ARG"), ((True, 1, 0, 4, 0, 0, True), "INVALID_ARG"),
+    ((True, 1, 8, 0, 0, 0, True), "INVALID_ARG"), ((True, 1, 8, 4, -1, 0, True), "INVALID_ARG"),
+    ((True, 1, 8, 4, 0, -1, True), "INVALID_ARG"), ((True, 1, 8, 4, 3, 2, True), "INVALID_ARG"),
+    ((True, 1, 8, 1 << 30, 1 << 30, 1 << 30, True), "INVALID_ARG"),
+    ((True, 65536, 8, 4, 0, 0, True), "UNSUPPORTED"), ((True, 1, 1 << 30, 4, 0, 0, True), "UNSUPPORTED"),
+    ((True, 1, 8, 1 << 30, 0, 0, True), "UNSUPPORTED"),
+])
+def test_select_refusals(hb, args, status):
+    acc, B, Nc, n_keep, first, last, keep = args
+    at = ctypes.c_void_p(4096)
+    assert hb._lib.hyb_evict_select(at if acc else None, B, Nc, None, n_keep, first, last, at if keep else None,
+                                    None) == getattr(hb, "HYB_ERR_" + status)
+
+
+def test_compact_refusals(hb):
+    p = hb.problem(B=2, Lq=1, Lkv=0, Hq=2, Hkv=2, d=64, m=4, W=8, Nc=16, di=64)
+    v = ctypes.c_void_p
+    kv, ki, ac = 2 * 16 * 2 * 64 * 2, 2 * 16 * 64 * 2, 2 * 16 * 4          # bytes of each input
+    base, out = 1 << 20, 1 << 24                                           # far apart, never read
+    good = dict(keep=1 << 16, n_keep=8, No=8, kc=base, vc=base + kv, kic=base + 2 * kv, acc=base + 2 * kv + ki,
+                kc_out=out, vc_out=out + kv, kic_out=out + 2 * kv, acc_out=out + 2 * kv + ki)
+
+    def call(**kw):
+        a = dict(good, **kw)
+        ptr = [v(a[n]) if a[n] else None for n in ("kc", "vc", "kic", "acc", "kc_out", "vc_out", "kic_out", "acc_out")]
+        return hb._lib.hyb_cache_compact(ctypes.byref(p), v(a["keep"]) if a["keep"] else None, a["n_keep"], a["No"],
+                                         *ptr, None)
+
+    none = dict(kc=None, vc=None, kic=None, acc=None, kc_out=None, vc_out=None, kic_out=None, acc_out=None)
+    for bad in (dict(keep=None), dict(n_keep=0), dict(No=7), dict(kc_out=None), dict(acc=None), none,
+                dict(kc_out=base), dict(kc_out=base + kv - 4),             # on its input, or on the end of it
+                dict(vc_out=base),                                         # on another cache's input
+                dict(kc_out=out + kv), dict(acc_out=out + 4),              # on another output
+                dict(kc_out=1 << 16), dict(acc_out=(1 << 16) + 60),        # on the list of kept entries
+                dict(kc=base + 2), dict(acc_out=out + 2 * kv + ki + 2)):
+        assert call(**bad) == hb.HYB_ERR_INVALID_ARG, bad
+    assert call(No=1 << 30) == hb.HYB_ERR_UNSUPPORTED
+    p.Nc = 0
+    assert call() == hb.HYB_ERR_INVALID_ARG
+    p.Nc = 16
+    # 4-bit caches: codes and pairs come together
+    a = [v(base + i * (1 << 16)) for i in range(7)] + [v(out + i * (1 << 16)) for i in range(7)]
+    for i in (0, 1, 7, 8):
+        b = list(a)
+        b[i] = None
+        assert hb._lib.hyb_cache_compact_fp4(ctypes.byref(p), v(1 << 16), 8, 8, *b, None) == hb.HYB_ERR_INVALID_ARG
+
+
+def test_python_calls_of_the_eviction_check_shapes(hb):
+    p = hb.problem(B=2, Lq=1, Lkv=0, Hq=4, Hkv=2, d=64, m=4, W=0, Nc=4, di=64)
+    bf = dict(dtype=torch.bfloat16)
+    q, kc, lse = torch.zeros((2, 1, 4, 64), **bf), torch.zeros((2, 4, 2, 64), **bf), torch.zeros((2, 4, 1))
+    for bad in (dict(q=q[:1]), dict(kc=kc[:, :2]), dict(lse=lse.double()), dict(acc=torch.zeros((2, 5))),
+                dict(idx=torch.zeros((2, 1, 4), dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            hb.hyb_attn_weights(p, **{**dict(q=q, kc=kc, lse=lse), **bad})
+    with pytest.raises(ValueError):
+        hb.hyb_evict_select(torch.zeros((2, 4), dtype=torch.float64), 2)
+    with pytest.raises(ValueError):
+        hb.hyb_evict_select(torch.zeros((2, 4)), 2, n_valid=torch.zeros(2))
+    keep = torch.zeros((2, 3), dtype=torch.int32)
+    for bad in (dict(keep=keep.long()), dict(keep=keep[:1]), dict(kc=kc[..., :32]), dict(kc=None, kc_out=kc),
+                dict(kc=kc.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            hb.hyb_cache_compact(p, **{**dict(keep=keep, kc=kc), **bad})
