@@ -12,8 +12,8 @@
 // sequence), the rest by each sequence's rows, and long key ranges are split
 // over CTAs; prefix_combine_kernel joins the parts.
 //
-// Work item = one 128-key tile stream (a split of the shared entries, or of one
-// sequence's own entries followed by its window) and two query tiles:
+// Work item = one stream of 128-key tiles (a piece of the shared entries, or of
+// one sequence's own entries followed by its window) and two query tiles:
 //   pair       two 128-row query tiles read the same keys (MMA-bound: K / V
 //              tiles are fetched once for 256 rows);
 //   alternate  where there is a single query tile, the two softmax warpgroups
@@ -22,15 +22,51 @@
 // A query tile holds hpt heads of one KV group x tpt tokens (hpt = min(g, 128),
 // tpt = 128 / hpt), fetched by one TMA box; rows past hpt * tpt are not used.
 //
-// Roles (384 threads) as in the dense prefill kernel: warps 0-3 / 4-7 softmax
-// and epilogue of query tile A / B (thread = TMEM lane = query row), warp 8 TMA
-// producer (K and V rings of two 32 KB stages each), warp 9 MMA issue, all lanes
-// active: it also zeroes, in shared memory, the V rows of a tile that no query
-// of the item sees, so that whatever such cache rows hold (0 x NaN = NaN)
-// never enters O.  Masked scores are replaced, not added to, for the same reason.
+// Roles (384 threads):
+//   warps 0-3   softmax + epilogue of query tile (or key stream) A, warps 4-7 of
+//               B: one thread per TMEM lane (= query row).
+//   warp 8      TMA producer (K and V rings of two 32 KB stages each).
+//   warps 9, 10 MMA issue for A and for B.  One thread for both left the tensor
+//               pipe idle while it walked from barrier to barrier (a key tile of
+//               a pair took 4650 clocks, 2048 of them MMAs); with a warp each the
+//               two chains only meet in the tensor pipe.  They also zero, in shared memory, the
+//               V rows of a tile that no query of the item sees, so that whatever
+//               such cache rows hold (0 x NaN = NaN) never enters O.  Masked
+//               scores are replaced, not added to, for the same reason.
+//   warp 11     works out the items (the positions of an item's tokens decide how
+//               many keys it has) three ahead, so that no role waits for global
+//               loads between items.
+// The softmax loops over 64-column halves instead of unrolling the tile: short
+// items run through the code once, and its instruction fetches were what they
+// waited for.
 #include "common.cuh"
 
 namespace hyb {
+
+// Bounded wait that tries the barrier some times before it looks at the clock
+// and the limit (a load from global memory, several hundred clocks): the waits
+// of these kernels are short and many.  Gives up when the CTA's abort flag is
+// up, like mbar_wait, which takes over afterwards.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
+    for (int it = 0; it < 64; ++it) {
+        if (mbar_try_wait(addr, parity))
+            return true;
+        if (*abort_flag)
+            return false;
+    }
+    return mbar_wait(bar, parity, abort_flag);
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t pred;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+    return pred != 0;
+}
 
 constexpr int kPfThreads = 384;
 constexpr int kPfSoftmaxRegs = 208;   // 2 x 128 x 208 + 128 x 88 = 384 x 168 (the launch budget)
@@ -38,18 +74,25 @@ constexpr int kPfOtherRegs = 88;
 constexpr int kPfBM = 128;
 constexpr int kPfBN = 128;
 constexpr int kPfStages = 2;
+constexpr int kPfItemSlots = 3;
 // The split is planned for this many SMs on every device, so that the workspace
 // size is a function of the problem alone.
 constexpr int kPfPlanSMs = 148;
+constexpr int kPfPairCost = 14, kPfAltCost = 12, kPfItemCost = 20;    // 1/8 us, see prefix_plan
 
 struct PrefixParams {
     int B, Lq, Lkv, Hq, Hkv, g, Np, Nc, m, W;
     int hpt, tpt, nht;            // heads and tokens of a query tile, head tiles of a KV group
-    int p_tiles, p_units, p_ns;   // shared entries: query tiles per KV head, items per KV head, splits
-    int o_tiles, o_units, o_ns;   // own keys: the same per sequence and KV head
+    int p_tiles, p_units;         // shared entries: query tiles and items per KV head
+    int o_tiles, o_units;         // own keys: the same per sequence and KV head
     int p_pair, o_pair;           // 1: pair, 0: alternate
-    int p_parts, n_parts;         // partial results per row: of the shared entries, in all
-    int n_items_p, n_items;
+    int p_ns, p_pieces;           // shared entries: pieces of an item's keys, pieces in all
+    // Own keys, as one stream of items of o_len units each (o_over of them stand
+    // for an item's cost beside its tiles): CTAs below o_rem, which have one
+    // piece of the shared entries more, take o_a units each, the others o_b.
+    int o_len, o_over, o_rem, o_a, o_b, o_total;
+    int ctas, ctas_used;          // planned for, and with work
+    int p_parts, n_parts;         // partial results per row: of the shared entries, in all (upper bound)
     long long rows;               // B * Lq * Hq
     float scale_log2;
     const int32_t *q_pos, *kv_pos0;
@@ -59,35 +102,46 @@ struct PrefixParams {
     float *lse;                   // [B, Hq, Lq] or NULL
 };
 
-template <int D>
-struct PrefixSmem {
-    static constexpr int Q_BYTES = kPfBM * D * 2;
-    static constexpr int KV_BYTES = kPfBN * D * 2;
-    static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = 2 * Q_BYTES;
-    static constexpr int OFF_V = OFF_K + kPfStages * KV_BYTES;
-    static constexpr int OFF_BAR = OFF_V + kPfStages * KV_BYTES;
-    static constexpr int OFF_MISC = OFF_BAR + 32 * 8;
-    static constexpr int BYTES = OFF_MISC + 16 * 4;
-};
-
-// barrier slots (two each from PB_KF on)
-enum { PB_QF = 0, PB_QE = 1, PB_KF = 2, PB_KE = 4, PB_VF = 6, PB_VE = 8, PB_SF = 10, PB_PF = 12, PB_OF = 14,
-       PB_OE = 16, PB_DONE = 18 };
-
+// A work item, as the roles read it from shared memory.
 struct PrefixItem {
-    bool pre, pair;      // shared entries?  two query tiles?
+    int last;            // 1: no further item
+    int pre, pair;       // shared entries?  two query tiles?
     int b, kvh, part;    // sequence (own keys), KV head, first partial result
     int tok0[2], h0[2];  // first token (of the batch's B * Lq, or of the sequence) and head of each query tile
-    bool val[2];         // warpgroup has work
+    int val1;            // the second query tile exists (pair)
     int ntok;            // tokens of the range tok0 counts in
     int nent;            // entries that some row of the item sees
     int rlo, nraw;       // first raw row and number of raw rows that some row sees
     int nte;             // entry tiles before the raw tiles
-    int t0, nt;          // first key tile and number of key tiles of this split
-    int nsteps;
-    long long kv0;
+    int t0, nt;          // first key tile and number of key tiles of this piece
 };
+
+// What one token of an item sees.
+struct PrefixToken {
+    int nv;              // entries
+    int wlo, whi;        // raw rows
+};
+
+template <int D>
+struct PrefixSmem {
+    static constexpr int Q_BYTES = kPfBM * D * 2;
+    static constexpr int KV_BYTES = kPfBN * D * 2;
+    static constexpr int STAGE_BYTES = 32 * 64;                        // per softmax warp: 32 rows x 16 channels
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = 2 * Q_BYTES;
+    static constexpr int OFF_V = OFF_K + kPfStages * KV_BYTES;
+    static constexpr int OFF_ST = OFF_V + kPfStages * KV_BYTES;
+    static constexpr int OFF_TOK = OFF_ST + 8 * STAGE_BYTES;
+    static constexpr int OFF_ITEM = OFF_TOK + kPfItemSlots * 256 * (int)sizeof(PrefixToken);
+    static constexpr int OFF_BAR = (OFF_ITEM + kPfItemSlots * (int)sizeof(PrefixItem) + 15) / 16 * 16;
+    static constexpr int OFF_MISC = OFF_BAR + 32 * 8;
+    static constexpr int BYTES = OFF_MISC + 16 * 4;
+};
+static_assert(1024 + PrefixSmem<128>::BYTES <= 227 * 1024, "shared memory of a CTA");
+
+// barrier slots (two each from PB_KF on, three item slots)
+enum { PB_QF = 0, PB_QE = 1, PB_KF = 2, PB_KE = 4, PB_VF = 6, PB_VE = 8, PB_SF = 10, PB_PF = 12, PB_OF = 14,
+       PB_OE = 16, PB_IF = 18, PB_IE = 21, PB_DONE = 24 };
 
 // Entries visible to position pos: those ending before its window.
 __device__ __forceinline__ int pf_visible(long long pos, int m, int W, int n)
@@ -100,88 +154,100 @@ __device__ __forceinline__ int pf_visible(long long pos, int m, int W, int n)
     return v < (unsigned long long)n ? (int)v : n;
 }
 
-__device__ __forceinline__ int pf_pos(const PrefixParams &p, int flat)
+// First unit of CTA k's share of the own-key stream, and the CTA a unit is in.
+__host__ __device__ __forceinline__ int pf_share(const PrefixParams &p, int k)
 {
-    return p.q_pos ? p.q_pos[flat] : flat % p.Lq;
+    const long long u = k < p.o_rem ? (long long)k * p.o_a
+                                    : (long long)p.o_rem * p.o_a + (long long)(k - p.o_rem) * p.o_b;
+    return u < p.o_total ? (int)u : p.o_total;
 }
 
-// The item w, computed by a whole warp (the positions of its tokens decide how
-// many keys there are).
-template <int D>
-__device__ __forceinline__ PrefixItem prefix_item(const PrefixParams &p, int w, int lane)
+__host__ __device__ __forceinline__ int pf_cta(const PrefixParams &p, int u)
+{
+    const int head = p.o_rem * p.o_a;
+    return u < head ? u / p.o_a : p.o_rem + (u - head) / p.o_b;
+}
+
+// Key tiles before unit u of an item of T tiles.
+__device__ __forceinline__ int pf_cut(const PrefixParams &p, int T, int u)
+{
+    return (int)((long long)T * max(u - p.o_over, 0) / (p.o_len - p.o_over));
+}
+
+// Works out one item (whole warp): piece `s` of p_ns of the shared entries for
+// item i, or units [u0, u1) of own-key item i.
+__device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int i, int s, int u0, int u1, int lane,
+                                            PrefixItem &out, PrefixToken *tokens)
 {
     PrefixItem it;
-    it.pre = w < p.n_items_p;
-    int units, s, ns, u;
-    if (it.pre) {
-        units = p.p_units;
-        ns = p.p_ns;
-        it.pair = p.p_pair != 0;
-        u = w % units;
-        const int r = w / units;
-        it.kvh = r % p.Hkv;
-        s = r / p.Hkv;
+    it.last = 0;
+    it.pre = pre;
+    int u;
+    if (pre) {
+        it.pair = p.p_pair;
+        u = i % p.p_units;
+        it.kvh = i / p.p_units;
         it.b = 0;
         it.part = it.pair ? s : 2 * s;
         it.ntok = p.B * p.Lq;
-        it.kv0 = 0;
     } else {
-        w -= p.n_items_p;
-        units = p.o_units;
-        ns = p.o_ns;
-        it.pair = p.o_pair != 0;
-        s = w % ns;
-        int r = w / ns;
-        u = r % units;
-        r /= units;
+        it.pair = p.o_pair;
+        u = i % p.o_units;
+        const int r = i / p.o_units;
         it.kvh = r % p.Hkv;
         it.b = r / p.Hkv;
         it.part = p.p_parts + (it.pair ? s : 2 * s);
         it.ntok = p.Lq;
-        it.kv0 = p.kv_pos0 ? p.kv_pos0[it.b] : 0;
     }
-    int pmax = INT_MIN, pmin = INT_MAX;
+    const long long kv0 = !pre && p.kv_pos0 ? p.kv_pos0[it.b] : 0;
+    const int tiles = pre ? p.p_tiles : p.o_tiles;
+    int nmax = 0, rlo = INT_MAX, rhi = -1;
+    it.val1 = 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int tile = it.pair ? 2 * u + x : u;
-        it.val[x] = tile < (it.pre ? p.p_tiles : p.o_tiles);
         it.tok0[x] = (tile / p.nht) * p.tpt;
         it.h0[x] = it.kvh * p.g + (tile % p.nht) * p.hpt;
-        if (!it.val[x])
+        if (tile >= tiles || (x == 1 && !it.pair))
             continue;
-        const int end = min(it.tok0[x] + p.tpt, it.ntok);
-        for (int t = it.tok0[x] + lane; t < end; t += 32) {
-            const int pos = pf_pos(p, it.pre ? t : it.b * p.Lq + t);
-            pmax = max(pmax, pos);
-            pmin = min(pmin, pos);
+        it.val1 = x;
+        for (int t = lane; t < p.tpt; t += 32) {
+            PrefixToken tk = {0, 0, -1};
+            if (it.tok0[x] + t < it.ntok) {
+                const int flat = (pre ? 0 : it.b * p.Lq) + it.tok0[x] + t;
+                const long long pos = p.q_pos ? p.q_pos[flat] : flat % p.Lq;
+                const int nv = pf_visible(pos, p.m, p.W, p.Np + p.Nc);
+                tk.nv = pre ? min(nv, p.Np) : max(nv - p.Np, 0);
+                nmax = max(nmax, tk.nv);
+                if (!pre && p.W > 0) {
+                    const long long lo = max(0ll, max(0ll, pos - p.W + 1) - kv0);
+                    const long long hi = min((long long)p.Lkv - 1, pos - kv0);
+                    if (hi >= lo) {
+                        tk.wlo = (int)lo;
+                        tk.whi = (int)hi;
+                        rlo = min(rlo, tk.wlo);
+                        rhi = max(rhi, tk.whi);
+                    }
+                }
+            }
+            tokens[x * 128 + t] = tk;
         }
     }
-    pmax = __reduce_max_sync(0xffffffffu, pmax);
-    pmin = __reduce_min_sync(0xffffffffu, pmin);
-    const int nv = pf_visible(pmax, p.m, p.W, p.Np + p.Nc);
-    it.nent = it.pre ? min(nv, p.Np) : max(nv - p.Np, 0);
+    it.nent = __reduce_max_sync(0xffffffffu, nmax);
+    it.rlo = __reduce_min_sync(0xffffffffu, rlo);
+    rhi = __reduce_max_sync(0xffffffffu, rhi);
+    it.nraw = rhi >= 0 ? rhi - it.rlo + 1 : 0;
     it.nte = (it.nent + kPfBN - 1) / kPfBN;
-    it.rlo = it.nraw = 0;
-    if (!it.pre && p.W > 0) {
-        const long long lo = max(0ll, max(0ll, (long long)pmin - p.W + 1) - it.kv0);
-        const long long hi = min((long long)p.Lkv - 1, (long long)pmax - it.kv0);
-        if (hi >= lo) {
-            it.rlo = (int)lo;
-            it.nraw = (int)(hi - lo + 1);
-        }
-    }
     const int T = it.nte + (it.nraw + kPfBN - 1) / kPfBN;
-    it.t0 = (int)((long long)T * s / ns);
-    it.nt = (int)((long long)T * (s + 1) / ns) - it.t0;
-    it.nsteps = it.pair ? it.nt : (it.nt + 1) / 2;
-    return it;
-}
-
-// Key tile that warpgroup x works on in step i (relative to t0), or -1.
-__device__ __forceinline__ int pf_tile(const PrefixItem &it, int i, int x)
-{
-    const int t = it.pair ? i : 2 * i + x;
-    return i >= 0 && it.val[x] && t < it.nt ? t : -1;
+    if (pre) {
+        it.t0 = (int)((long long)T * s / p.p_ns);
+        it.nt = (int)((long long)T * (s + 1) / p.p_ns) - it.t0;
+    } else {
+        it.t0 = pf_cut(p, T, u0);
+        it.nt = (u1 == p.o_len ? T : pf_cut(p, T, u1)) - it.t0;
+    }
+    if (lane == 0)
+        out = it;
 }
 
 template <int D>
@@ -192,8 +258,6 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                    const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_vr,
                    const PrefixParams p)
 {
-    pdl_wait();      // launched as a programmatic dependent: the previous kernel's writes
-    pdl_trigger();   // are visible from here on; the next kernel may start its launch
     using SM = PrefixSmem<D>;
     constexpr int NCB = D / 64;
     extern __shared__ __align__(1024) uint8_t pf_smem_raw[];
@@ -202,6 +266,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
     uint8_t *sQ = smem + SM::OFF_Q;
     uint8_t *sK = smem + SM::OFF_K;
     uint8_t *sV = smem + SM::OFF_V;
+    PrefixToken *sTok = reinterpret_cast<PrefixToken *>(smem + SM::OFF_TOK);
+    PrefixItem *sItem = reinterpret_cast<PrefixItem *>(smem + SM::OFF_ITEM);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + SM::OFF_BAR);
     int *misc = reinterpret_cast<int *>(smem + SM::OFF_MISC);
     volatile int *abort_flag = misc + 1;
@@ -210,18 +276,22 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
 
     if (threadIdx.x == 0) {
         mbar_init(&bar[PB_QF], 1);
-        mbar_init(&bar[PB_QE], 1);
+        mbar_init(&bar[PB_QE], 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar[PB_KF + s], 1);
-            mbar_init(&bar[PB_KE + s], 1);
+            mbar_init(&bar[PB_KE + s], 2);     // a commit of each MMA warp, or two of the one that uses it
             mbar_init(&bar[PB_VF + s], 1);
-            mbar_init(&bar[PB_VE + s], 1);
+            mbar_init(&bar[PB_VE + s], 2);
             mbar_init(&bar[PB_SF + s], 1);
-            mbar_init(&bar[PB_PF + s], 128);
+            mbar_init(&bar[PB_PF + s], 4);     // one arrival a warp
             mbar_init(&bar[PB_OF + s], 1);
-            mbar_init(&bar[PB_OE + s], 128);
+            mbar_init(&bar[PB_OE + s], 4);
         }
-        mbar_init(&bar[PB_DONE], 1);
+        for (int s = 0; s < kPfItemSlots; ++s) {
+            mbar_init(&bar[PB_IF + s], 1);
+            mbar_init(&bar[PB_IE + s], 11);    // producer, MMA and softmax warps
+        }
+        mbar_init(&bar[PB_DONE], 2);
         mbar_fence_init();
         misc[1] = 0;
     }
@@ -231,27 +301,80 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[0];
-    constexpr uint32_t TM_S[2] = {0, kPfBN};
-    constexpr uint32_t TM_O[2] = {2 * kPfBN, 2 * kPfBN + 128};
-    if (warp == 8) {
+    pdl_wait();      // launched as a programmatic dependent: the previous kernel's writes
+    pdl_trigger();   // are visible from here on; the next kernel may start its launch
+    // every lane waits; the warp goes on only if all of them got through
+    auto wait = [&](int b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_short(&bar[b], parity, abort_flag)) != 0;
+    };
+    // the n-th item of this CTA (false: none, or giving up); `release` after its last read
+    auto item = [&](uint32_t n, PrefixItem &it) {
+        if (!wait(PB_IF + n % kPfItemSlots, (n / kPfItemSlots) & 1))
+            return false;
+        it = sItem[n % kPfItemSlots];
+        return it.last == 0;
+    };
+    auto release = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&bar[PB_IE + n % kPfItemSlots]);
+    };
+
+    constexpr uint32_t TM_O = 2 * kPfBN;         // S_A, S_B, then O_A, O_B (128 columns each)
+    if (warp >= 8)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfOtherRegs));
+    if (warp == 11) {
+        // ================================ items ================================
+        uint32_t n = 0;
+        bool ok = true;
+        auto next = [&](bool pre, int i, int s, int u0, int u1) {
+            const uint32_t slot = n % kPfItemSlots;
+            if (n >= kPfItemSlots && !wait(PB_IE + slot, (n / kPfItemSlots - 1) & 1))
+                return false;
+            if (i < 0) {
+                if (lane == 0)
+                    sItem[slot].last = 1;
+            } else {
+                prefix_item(p, pre, i, s, u0, u1, lane, sItem[slot], sTok + slot * 256);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[PB_IF + slot]);
+            ++n;
+            return true;
+        };
+        // pieces of the shared entries: the items of one KV head and piece number
+        // lie side by side, so that they read the same tiles at the same time
+        for (int q = blockIdx.x; ok && q < p.p_pieces; q += p.ctas) {
+            const int u = q % p.p_units, r = q / p.p_units;
+            ok = next(true, (r / p.p_ns) * p.p_units + u, r % p.p_ns, 0, 0);
+        }
+        const int end = p.o_total > 0 ? pf_share(p, blockIdx.x + 1) : 0;
+        for (int u = p.o_total > 0 ? pf_share(p, blockIdx.x) : 0; ok && u < end;) {
+            const int i = u / p.o_len, u0 = u - i * p.o_len, u1 = min(p.o_len, u0 + (end - u));
+            ok = next(false, i, (int)blockIdx.x - pf_cta(p, i * p.o_len), u0, u1);
+            u += u1 - u0;
+        }
+        if (ok)
+            next(false, -1, 0, 0, 0);
+    } else if (warp == 8) {
         // ================================ producer ================================
         const uint32_t q_bytes = (uint32_t)p.hpt * p.tpt * D * 2;
-        uint32_t kc = 0, vc = 0, nq = 0;
+        uint32_t kc = 0, vc = 0, nq = 0, qn = 0;
         bool ok = true;
-        for (int w = blockIdx.x; ok && w < p.n_items; w += gridDim.x) {
-            const PrefixItem it = prefix_item<D>(p, w, lane);
+        PrefixItem it;
+        while (ok && item(nq, it)) {
+            release(nq);
             if (lane == 0) {
-                if (nq > 0 && !mbar_wait(&bar[PB_QE], (nq - 1) & 1, abort_flag))
-                    ok = false;
+                ok = nq == 0 || mbar_wait_short(&bar[PB_QE], (nq - 1) & 1, abort_flag);
                 if (ok) {
-                    const int nqt = it.pair && it.val[1] ? 2 : 1;
-                    mbar_arrive_expect_tx(&bar[PB_QF], nqt * q_bytes);
-                    for (int x = 0; x < nqt; ++x)
-                        for (int cb = 0; cb < NCB; ++cb)
+                    mbar_arrive_expect_tx(&bar[PB_QF], (1 + it.val1) * q_bytes);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        for (int cb = 0; x <= it.val1 && cb < NCB; ++cb)
                             tma_load_4d(sQ + x * SM::Q_BYTES + cb * kPfBM * 128, it.pre ? &tm_qp : &tm_qo,
-                                        &bar[PB_QF], cb * 64, it.h0[x], it.tok0[x], it.pre ? 0 : it.b);
-                    ++nq;
+                                        &bar[PB_QF], cb * 64, it.h0[x], it.tok0[x], it.b);
+                    ++qn;
                 }
                 const int per = it.pair ? 1 : 2;   // key tiles of a step
                 for (int i = 0; ok && i < it.nt; i += per) {
@@ -267,305 +390,318 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                                                         : (!ent ? &tm_kr : it.pre ? &tm_kp : &tm_kc);
                             const uint32_t st = cnt % kPfStages;
                             if (cnt >= kPfStages &&
-                                !mbar_wait(&empty[st], ((cnt / kPfStages) - 1) & 1, abort_flag)) {
+                                !mbar_wait_short(&empty[st], ((cnt / kPfStages) - 1) & 1, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            // The MMA warps wait for full stages by parity, and an item's
+                            // first tiles may follow tiles that only the other warp waited
+                            // for: K of tile n goes out once V of tile n - 2 has landed (K
+                            // has, since Q was reloaded), so that a warp that has seen K of
+                            // tile n is at most one phase of V behind.
+                            if (!kv && j < 2 && cnt >= kPfStages &&
+                                !mbar_wait_short(&bar[PB_VF + st], ((cnt / kPfStages) - 1) & 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
                             mbar_arrive_expect_tx(&full[st], SM::KV_BYTES);
                             for (int cb = 0; cb < NCB; ++cb)
                                 tma_load_4d(ring + st * SM::KV_BYTES + cb * kPfBN * 128, map, &full[st], cb * 64,
-                                            it.kvh, row0, it.pre ? 0 : it.b);
+                                            it.kvh, row0, it.b);
                             ++cnt;
                         }
                     }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (ok)
+                ++nq;
         }
         if (lane == 0) {
             // unwinding: wait for the last copies issued into every slot
-            if (nq > 0)
-                drain_wait(&bar[PB_QF], (nq - 1) & 1);
+            if (qn > 0)
+                drain_wait(&bar[PB_QF], (qn - 1) & 1);
             for (uint32_t c = (kc > kPfStages ? kc - kPfStages : 0); c < kc; ++c)
                 drain_wait(&bar[PB_KF + c % kPfStages], (c / kPfStages) & 1);
             for (uint32_t c = (vc > kPfStages ? vc - kPfStages : 0); c < vc; ++c)
                 drain_wait(&bar[PB_VF + c % kPfStages], (c / kPfStages) & 1);
         }
-    } else if (warp == 9) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfOtherRegs));
+    } else if (warp >= 8) {
         // ================================ MMA issue ================================
+        const int x = warp - 9;
         const uint32_t idesc_qk = idesc_bf16(kPfBM, kPfBN, false, false);
         const uint32_t idesc_pv = idesc_bf16(kPfBM, D, false, true);
-        const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
-        uint32_t kc = 0, vc = 0, nq = 0;
-        uint32_t pcnt[2] = {0, 0};
+        const uint32_t aK = smem_u32(sK), aV = smem_u32(sV);
+        const uint32_t tS = tmem + x * kPfBN, tO = tmem + TM_O + x * 128;
+        const bool leader = elect_one();
+        uint32_t base = 0;            // key tiles of the items before this one
+        uint32_t pcnt = 0, ocnt = 0, nq = 0;
         bool ok = true;
-        // every lane waits; the warp goes on only if all of them got through
-        auto wait = [&](int b, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(&bar[b], parity, abort_flag)) != 0;
-        };
-        for (int w = blockIdx.x; ok && w < p.n_items; w += gridDim.x) {
-            const PrefixItem it = prefix_item<D>(p, w, lane);
-            ok = wait(PB_QF, nq & 1);
-            bool first_pv[2] = {true, true};
-            bool waited_oe = nq == 0;
-            for (int i = 0; ok && i <= it.nsteps; ++i) {
-                for (int x = 0; ok && x < 2; ++x) {
-                    const int tp = pf_tile(it, i - 1, x);
-                    const int tc = i < it.nsteps ? pf_tile(it, i, x) : -1;
-                    // stages are waited for by the first user of a tile
-                    const bool first_use = !it.pair || x == 0;
-                    if (tp >= 0) {
-                        const uint32_t vs = vc % kPfStages;
-                        if (first_use) {
-                            if (!(ok = wait(PB_VF + vs, (vc / kPfStages) & 1)))
-                                break;
-                            const int t = it.t0 + tp;
-                            const int seen = t < it.nte ? it.nent - t * kPfBN : it.nraw - (t - it.nte) * kPfBN;
-                            if (seen < kPfBN) {
-                                // rows that no query of the item sees take no part, whatever they hold
-                                for (int cb = 0; cb < NCB; ++cb)
-                                    for (int c = seen * 8 + lane; c < kPfBN * 8; c += 32)
-                                        *reinterpret_cast<uint4 *>(sV + vs * SM::KV_BYTES + cb * kPfBN * 128 +
-                                                                   c * 16) = make_uint4(0, 0, 0, 0);
-                                fence_proxy_async_smem();
-                                __syncwarp();
-                            }
-                        }
-                        if (!waited_oe) {
-                            // both epilogues of the previous item have read O
-                            if (!(ok = wait(PB_OE + 0, (nq - 1) & 1) && wait(PB_OE + 1, (nq - 1) & 1)))
-                                break;
-                            waited_oe = true;
-                        }
-                        if (!(ok = wait(PB_PF + x, pcnt[x] & 1)))
-                            break;
-                        ++pcnt[x];
-                        tc_fence_after();
-                        if (lane == 0) {
-#pragma unroll
-                            for (int kk = 0; kk < kPfBN / 16; ++kk) {
-                                const uint64_t db = sw128_desc(aV + vs * SM::KV_BYTES + kk * 16 * 128,
-                                                               kPfBN * 128, 1024);
-                                mma_bf16_ts(tmem + TM_O[x], tmem + TM_S[x] + kk * 8, db, idesc_pv,
-                                            (first_pv[x] && kk == 0) ? 0u : 1u);
-                            }
-                        }
-                        first_pv[x] = false;
-                        if (!it.pair || x == 1 || !it.val[1]) {
-                            if (lane == 0)
-                                mma_commit(&bar[PB_VE + vs]);
-                            ++vc;
-                        }
+        PrefixItem it;
+        while (item(nq, it)) {
+            release(nq);
+            // this warp's key tiles: all of a pair's, or every second one
+            const int step = it.pair ? 1 : 2, first = it.pair ? (x <= it.val1 ? 0 : it.nt) : x;
+            const uint32_t aQ = smem_u32(sQ) + (it.pair ? x : 0) * SM::Q_BYTES;
+            if (!(ok = wait(PB_QF, nq & 1)))
+                break;
+            // O is free once the epilogue of this warp's previous item with keys has
+            // read it (items without keys for it have no epilogue to wait for)
+            bool o_free = ocnt == 0;
+            const bool alone = !it.pair || !it.val1;   // no other warp reads this one's tiles
+            for (int t = first; t < it.nt + step; t += step) {
+                if (t > first) {
+                    const uint32_t n = base + t - step, vs = n % kPfStages;
+                    if (!(ok = wait(PB_VF + vs, (n / kPfStages) & 1)))
+                        break;
+                    const int kt = it.t0 + t - step;
+                    const int seen = kt < it.nte ? it.nent - kt * kPfBN : it.nraw - (kt - it.nte) * kPfBN;
+                    if (seen < kPfBN) {
+                        // rows that no query of the item sees take no part, whatever they hold
+                        for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll 1
+                            for (int c = seen * 8 + lane; c < kPfBN * 8; c += 32)
+                                *reinterpret_cast<uint4 *>(sV + vs * SM::KV_BYTES + cb * kPfBN * 128 + c * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    if (tc >= 0) {
-                        const uint32_t ks = kc % kPfStages;
-                        if (first_use && !(ok = wait(PB_KF + ks, (kc / kPfStages) & 1)))
-                            break;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t a = aQ + (it.pair ? x : 0) * SM::Q_BYTES;
+                    if (!o_free && !(ok = wait(PB_OE + x, (ocnt - 1) & 1)))
+                        break;
+                    o_free = true;
+                    if (!(ok = wait(PB_PF + x, pcnt & 1)))
+                        break;
+                    ++pcnt;
+                    tc_fence_after();
+                    if (leader) {
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint64_t da = sw128_desc(a + (kk >> 2) * kPfBM * 128 + (kk & 3) * 32, 16,
-                                                               1024);
-                                const uint64_t db = sw128_desc(aK + ks * SM::KV_BYTES + (kk >> 2) * kPfBN * 128 +
-                                                                   (kk & 3) * 32,
-                                                               16, 1024);
-                                mma_bf16_ss(tmem + TM_S[x], da, db, idesc_qk, kk > 0 ? 1u : 0u);
-                            }
-                            mma_commit(&bar[PB_SF + x]);
+                        for (int kk = 0; kk < kPfBN / 16; ++kk) {
+                            const uint64_t db = sw128_desc(aV + vs * SM::KV_BYTES + kk * 16 * 128, kPfBN * 128, 1024);
+                            mma_bf16_ts(tO, tS + kk * 8, db, idesc_pv, (t == first + step && kk == 0) ? 0u : 1u);
                         }
-                        if (!it.pair || x == 1 || !it.val[1]) {
-                            if (lane == 0)
-                                mma_commit(&bar[PB_KE + ks]);
-                            ++kc;
-                        }
+                        mma_commit(&bar[PB_VE + vs]);
+                        if (alone)
+                            mma_commit(&bar[PB_VE + vs]);
                     }
                 }
-                if (ok && lane == 0 && (i == it.nsteps - 1 || it.nsteps == 0))
-                    mma_commit(&bar[PB_QE]);
+                if (t < it.nt) {
+                    const uint32_t n = base + t, ks = n % kPfStages;
+                    if (!(ok = wait(PB_KF + ks, (n / kPfStages) & 1)))
+                        break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t da = sw128_desc(aQ + (kk >> 2) * kPfBM * 128 + (kk & 3) * 32, 16, 1024);
+                            const uint64_t db = sw128_desc(aK + ks * SM::KV_BYTES + (kk >> 2) * kPfBN * 128 +
+                                                               (kk & 3) * 32,
+                                                           16, 1024);
+                            mma_bf16_ss(tS, da, db, idesc_qk, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(&bar[PB_SF + x]);
+                        mma_commit(&bar[PB_KE + ks]);
+                        if (alone)
+                            mma_commit(&bar[PB_KE + ks]);
+                        if (t + step >= it.nt)
+                            mma_commit(&bar[PB_QE]);
+                    }
+                }
             }
             if (!ok)
                 break;
-            if (!waited_oe &&   // one wait an item even without a PV
-                !(ok = wait(PB_OE + 0, (nq - 1) & 1) && wait(PB_OE + 1, (nq - 1) & 1)))
-                break;
-            if (lane == 0)
-                for (int x = 0; x < 2; ++x)
-                    if (!first_pv[x])
-                        mma_commit(&bar[PB_OF + x]);
+            if (leader)
+                mma_commit(&bar[first < it.nt ? PB_OF + x : PB_QE]);
+            ocnt += first < it.nt;
+            base += it.nt;
             ++nq;
         }
-        if (lane == 0) {
+        if (leader)
             mma_commit(&bar[PB_DONE]);
-            drain_wait(&bar[PB_DONE], 0);
-        }
-    } else if (warp >= 10) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfOtherRegs));
+        __syncwarp();
+        drain_wait(&bar[PB_DONE], 0);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfSoftmaxRegs));
         // ========================== softmax + epilogue ==========================
-        const int x = warp >> 2;            // 0: tile A, 1: tile B
+        const int x = warp >> 2;            // 0: A, 1: B
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t tS = tl + TM_S[x];
-        const uint32_t tO = tl + TM_O[x];
+        const uint32_t tS = tl + x * kPfBN;
+        const uint32_t tO = tl + TM_O + x * 128;
+        uint8_t *stage = smem + SM::OFF_ST + warp * SM::STAGE_BYTES;
         const int rtok = row / p.hpt, rhead = row % p.hpt;
-        uint32_t scnt = 0, ocnt = 0;
+        const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
+        uint32_t scnt = 0, ocnt = 0, nq = 0;
         bool ok = true;
-        for (int w = blockIdx.x; ok && w < p.n_items; w += gridDim.x) {
-            const PrefixItem it = prefix_item<D>(p, w, lane);
-            const int tok = it.tok0[x] + rtok;
-            const int h = it.h0[x] + rhead;
-            const bool valid_row = it.val[x] && rtok < p.tpt && tok < it.ntok && h < (it.kvh + 1) * p.g;
-            const int flat = it.pre ? tok : it.b * p.Lq + tok;
-            int nv = 0, wlo = 0, whi = -1;   // visible entries; window as raw rows wlo..whi
-            if (valid_row) {
-                const long long pos = pf_pos(p, flat);
-                nv = pf_visible(pos, p.m, p.W, p.Np + p.Nc);
-                nv = it.pre ? min(nv, p.Np) : max(nv - p.Np, 0);
-                if (it.nraw > 0) {
-                    wlo = (int)max(0ll, max(0ll, pos - p.W + 1) - it.kv0);
-                    whi = (int)min((long long)p.Lkv - 1, max(-1ll, pos - it.kv0));
-                }
-            }
+        PrefixItem it;
+        while (ok && item(nq, it)) {
+            const int step = it.pair ? 1 : 2, first = it.pair ? (x <= it.val1 ? 0 : it.nt) : x;
+            const int xt = it.pair ? x : 0;
+            const int tok = (xt ? it.tok0[1] : it.tok0[0]) + rtok;
+            const int h = (xt ? it.h0[1] : it.h0[0]) + rhead;
+            const bool valid_row = rtok < p.tpt && tok < it.ntok && h < (it.kvh + 1) * p.g && xt <= it.val1;
+            PrefixToken tk = {0, 0, -1};
+            if (valid_row)
+                tk = sTok[(nq % kPfItemSlots) * 256 + xt * 128 + rtok];
+            release(nq);
+            const bool warp_rows = __any_sync(0xffffffffu, valid_row);
+            const int flat = (it.pre ? 0 : it.b * p.Lq) + tok;
             float m_ref = -INFINITY, l_sum = 0.f;
-            bool any = false;
-            for (int i = 0; i < it.nsteps; ++i) {
-                const int tt = pf_tile(it, i, x);
-                if (tt < 0)
-                    continue;
-                // valid columns c_lo..c_hi of this key tile for this row
-                const int t = it.t0 + tt;
-                int c_lo = 0, c_hi;
-                if (t < it.nte) {
-                    c_hi = min(nv - 1 - t * kPfBN, kPfBN - 1);
-                } else {
-                    const int base = it.rlo + (t - it.nte) * kPfBN;
-                    c_lo = max(0, min(wlo - base, kPfBN));
-                    c_hi = max(-1, min(whi - base, kPfBN - 1));
-                }
-                const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == kPfBN - 1);
-                if (!__all_sync(0xffffffffu, mbar_wait(&bar[PB_SF + x], scnt & 1, abort_flag))) {
-                    ok = false;
+            for (int t = first; t < it.nt; t += step) {
+                if (!(ok = wait(PB_SF + x, scnt & 1)))
                     break;
-                }
                 ++scnt;
                 tc_fence_after();
-                float sv[kPfBN];
-#pragma unroll
-                for (int c = 0; c < kPfBN / 32; ++c)
-                    tmem_ld32(tS + c * 32, *reinterpret_cast<float(*)[32]>(&sv[c * 32]));
-                tmem_ld_wait();
-                if (!full) {
-#pragma unroll
-                    for (int c = 0; c < kPfBN; ++c)
-                        sv[c] = (c >= c_lo && c <= c_hi) ? sv[c] : -INFINITY;
-                }
-                // row max over eight independent 3-input max chains
-                float tmax;
-                {
-                    float mk[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float a = fmax3f(sv[16 * k], sv[16 * k + 1], sv[16 * k + 2]);
-#pragma unroll
-                        for (int q = 3; q < 15; q += 2)
-                            a = fmax3f(a, sv[16 * k + q], sv[16 * k + q + 1]);
-                        mk[k] = fmaxf(a, sv[16 * k + 15]);
+                if (warp_rows) {
+                    // columns c_lo .. c_lo + c_n of this key tile are visible to this row
+                    int c_lo = 0, c_hi;
+                    const int kt = it.t0 + t;
+                    if (kt < it.nte) {
+                        c_hi = min(tk.nv - 1 - kt * kPfBN, kPfBN - 1);
+                    } else {
+                        const int r0 = it.rlo + (kt - it.nte) * kPfBN;
+                        c_lo = max(0, tk.wlo - r0);
+                        c_hi = min(tk.whi - r0, kPfBN - 1);
                     }
-                    tmax = fmax3f(fmax3f(mk[0], mk[1], mk[2]), fmax3f(mk[3], mk[4], mk[5]),
-                                  fmaxf(mk[6], mk[7]));
-                }
-                tmax *= p.scale_log2;  // the scale is positive
-                // the reference maximum moves (and O is rescaled) only when a
-                // tile raises it by more than 2^8
-                float alpha = 1.f;
-                if (tmax > m_ref + 8.f) {
-                    alpha = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - tmax);
-                    m_ref = tmax;
-                    l_sum *= alpha;
-                }
-                if (any && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    // O holds every earlier PV (S_full covers all MMAs issued before this QK)
+                    const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == kPfBN - 1);
+                    if (c_hi < c_lo) {
+                        c_lo = 1 << 20;
+                        c_hi = c_lo;
+                    }
+                    const unsigned c_n = (unsigned)(c_hi - c_lo);
+                    // row maximum
+                    float tmax = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float ov[32];
-                        tmem_ld32(tO + c * 32, ov);
+                    for (int c = 0; c < kPfBN; c += 64) {
+                        float sv[64];
+                        tmem_ld32(tS + c, *reinterpret_cast<float(*)[32]>(&sv[0]));
+                        tmem_ld32(tS + c + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
                         tmem_ld_wait();
+                        if (!full) {
 #pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            ov[q] *= alpha;
-                        tmem_st32(tO + c * 32, ov);
+                            for (int q = 0; q < 64; ++q)
+                                sv[q] = (unsigned)(c + q - c_lo) <= c_n ? sv[q] : -INFINITY;
+                        }
+                        float mk[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float a = fmax3f(sv[16 * k], sv[16 * k + 1], sv[16 * k + 2]);
+#pragma unroll
+                            for (int q = 3; q < 15; q += 2)
+                                a = fmax3f(a, sv[16 * k + q], sv[16 * k + q + 1]);
+                            mk[k] = fmaxf(a, sv[16 * k + 15]);
+                        }
+                        tmax = fmax3f(tmax, fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
                     }
-                }
-                const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
-                // P = exp2(s * scale - mu), rounded to bf16 (the MMA operand; its
-                // relative error 2^-9 a term averages out below the output's own
-                // rounding) over the first 64 columns of S; the row sum is of the
-                // fp32 values
-                const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-                const uint64_t nmu2 = f2(-mu, -mu);
-                uint64_t lacc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                for (int c = 0; c < kPfBN / 32; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int q = 0; q < 32; q += 2) {
-                        float x0, x1;
-                        f2_split(fma_f2(f2(sv[c * 32 + q], sv[c * 32 + q + 1]), sc2, nmu2), x0, x1);
-                        const float e0 = ex2_approx(x0);
-                        const float e1 = ex2_approx(x1);
-                        lacc[(q >> 1) & 3] = add_f2(lacc[(q >> 1) & 3], f2(e0, e1));
-                        pk[q >> 1] = pack_bf16x2(e0, e1);
+                    tmax *= p.scale_log2;  // the scale is positive
+                    // the reference maximum moves (and O is rescaled) only when a
+                    // tile raises it by more than 2^8
+                    float alpha = 1.f;
+                    if (tmax > m_ref + 8.f) {
+                        alpha = (m_ref == -INFINITY) ? 0.f : ex2_approx(m_ref - tmax);
+                        m_ref = tmax;
+                        l_sum *= alpha;
                     }
-                    tmem_st16(tS + c * 16, pk);
-                }
-                {
-                    float a0, a1, b0, b1;
+                    if (t > first && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // O holds every earlier PV (S_full covers all MMAs issued before this QK)
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float ov[32];
+                            tmem_ld32(tO + c, ov);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int q = 0; q < 32; ++q)
+                                ov[q] *= alpha;
+                            tmem_st32(tO + c, ov);
+                        }
+                    }
+                    // P = exp2(s * scale - mu), rounded to bf16 (the MMA operand; its
+                    // relative error 2^-8 a term averages out below the output's own
+                    // rounding) over the first 64 columns of S; the row sum is of the
+                    // fp32 values.  Half 0's P lies over columns 0-31, which are read.
+                    const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
+                    const uint64_t nmu2 = f2(-mu, -mu);
+                    uint64_t lacc[2] = {0ull, 0ull};
+#pragma unroll 1
+                    for (int c = 0; c < kPfBN; c += 64) {
+                        float sv[64];
+                        tmem_ld32(tS + c, *reinterpret_cast<float(*)[32]>(&sv[0]));
+                        tmem_ld32(tS + c + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
+                        tmem_ld_wait();
+                        if (!full) {
+#pragma unroll
+                            for (int q = 0; q < 64; ++q)
+                                sv[q] = (unsigned)(c + q - c_lo) <= c_n ? sv[q] : -INFINITY;
+                        }
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int q = 0; q < 32; q += 2) {
+                                float x0, x1;
+                                f2_split(fma_f2(f2(sv[hh * 32 + q], sv[hh * 32 + q + 1]), sc2, nmu2), x0, x1);
+                                const float e0 = ex2_approx(x0);
+                                const float e1 = ex2_approx(x1);
+                                lacc[(q >> 1) & 1] = add_f2(lacc[(q >> 1) & 1], f2(e0, e1));
+                                pk[q >> 1] = pack_bf16x2(e0, e1);
+                            }
+                            tmem_st16(tS + (c >> 1) + hh * 16, pk);
+                        }
+                    }
+                    float a0, a1;
                     f2_split(add_f2(lacc[0], lacc[1]), a0, a1);
-                    f2_split(add_f2(lacc[2], lacc[3]), b0, b1);
-                    l_sum += (a0 + a1) + (b0 + b1);
+                    l_sum += a0 + a1;
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&bar[PB_PF + x]);
-                any = true;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bar[PB_PF + x]);
             }
             if (!ok)
                 break;
             // epilogue: this item's part of the row
-            if (any) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bar[PB_OF + x], ocnt & 1, abort_flag))) {
-                    ok = false;
+            if (first < it.nt) {
+                if (!(ok = wait(PB_OF + x, ocnt & 1)))
                     break;
-                }
                 ++ocnt;
                 tc_fence_after();
             }
-            const size_t at = (size_t)(it.part + (it.pair ? 0 : x)) * p.rows + (size_t)flat * p.Hq + h;
+            const long long at = (long long)(it.part + (it.pair ? 0 : x)) * p.rows + (long long)flat * p.Hq + h;
             if (valid_row)
                 p.part_ml[at] = make_float2(m_ref, l_sum);
-            if (any) {
-                const bool store = valid_row && l_sum != 0.f;
+            const unsigned stored = __ballot_sync(0xffffffffu, valid_row && l_sum != 0.f);
+            if (stored) {
+                // sixteen channels of the warp's rows at a time, through shared
+                // memory, so that a store instruction writes 64 bytes of eight rows
                 float *orow = p.part_o + at * D;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    float ov[32];
-                    tmem_ld32(tO + c * 32, ov);
+                for (int c = 0; c < D; c += 16) {
+                    float ov[16];
+                    tmem_ld16(tO + c, ov);
                     tmem_ld_wait();
-                    if (store) {
 #pragma unroll
-                        for (int q = 0; q < 32; q += 4)
-                            *reinterpret_cast<float4 *>(orow + c * 32 + q) =
-                                make_float4(ov[q], ov[q + 1], ov[q + 2], ov[q + 3]);
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<float4 *>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                            make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int r8 = 0; r8 < 32; r8 += 8) {
+                        const int r = r8 + (lane >> 2), q = lane & 3;
+                        float *dst = reinterpret_cast<float *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(orow), r));
+                        if ((stored >> r) & 1)
+                            *reinterpret_cast<float4 *>(dst + c + 4 * q) =
+                                *reinterpret_cast<const float4 *>(stage + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
                     }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
-            mbar_arrive(&bar[PB_OE + x]);
+            __syncwarp();
+            if (lane == 0 && first < it.nt)
+                mbar_arrive(&bar[PB_OE + x]);
+            ++nq;
         }
     }
 
@@ -577,56 +713,110 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
     }
 }
 
-// Joins the parts of each row: D / 4 lanes per row, four channels a lane.
-template <int D>
-__global__ void __launch_bounds__(256)
-prefix_combine_kernel(const PrefixParams p)
+// Joins the parts of each row: D / 4 lanes hold four channels each; with WAYS > 1
+// (few rows, many parts) as many lane groups take every WAYS-th part of a row and
+// meet in shared memory.
+template <int D, int WAYS>
+__global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams p)
 {
     pdl_wait();
     pdl_trigger();
     constexpr int LPR = D / 4;
-    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
+    constexpr int GROUPS = 256 / LPR;           // lane groups of the block
+    const int grp = threadIdx.x / LPR, way = grp % WAYS;
+    const long long row = (long long)blockIdx.x * (GROUPS / WAYS) + grp / WAYS;
     const int c = (threadIdx.x % LPR) * 4;
-    if (row >= p.rows)
+    const bool in = row < p.rows;
+    // this row's parts: [0, np) and [p_parts, p_parts + no)
+    int np = 0, no = 0;
+    long long b = 0, t = 0;
+    int h = 0;
+    if (in) {
+        const unsigned bt = (unsigned)row / (unsigned)p.Hq;     // rows fit 31 bits
+        h = (int)((unsigned)row - bt * (unsigned)p.Hq);
+        b = bt / (unsigned)p.Lq;
+        t = bt - (unsigned)b * (unsigned)p.Lq;
+        const int kvh = h / p.g, ht = (h - kvh * p.g) / p.hpt;
+        np = p.p_parts;
+        if (p.o_total > 0) {
+            const int tile = ((int)t / p.tpt) * p.nht + ht;
+            const int i = ((int)b * p.Hkv + kvh) * p.o_units + (p.o_pair ? tile >> 1 : tile);
+            no = pf_cta(p, (i + 1) * p.o_len - 1) - pf_cta(p, i * p.o_len) + 1;
+            no *= p.o_pair ? 1 : 2;
+        }
+    }
+    float M = -INFINITY, L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 4;                         // parts in flight
+    for (int i0 = way; i0 < np + no; i0 += U * WAYS) {
+        float2 ml[U];
+        float4 v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * WAYS;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (i < np + no)
+                ml[k] = p.part_ml[(size_t)(i < np ? i : p.p_parts + i - np) * p.rows + row];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * WAYS;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ml[k].y != 0.f)                  // a part without keys has no row
+                v[k] = *reinterpret_cast<const float4 *>(
+                    p.part_o + ((size_t)(i < np ? i : p.p_parts + i - np) * p.rows + row) * D + c);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (ml[k].y == 0.f)
+                continue;
+            const float m = fmaxf(M, ml[k].x);
+            const float w0 = exp2f(M - m), w1 = exp2f(ml[k].x - m);
+            M = m;
+            L = L * w0 + ml[k].y * w1;
+            a.x = a.x * w0 + v[k].x * w1;
+            a.y = a.y * w0 + v[k].y * w1;
+            a.z = a.z * w0 + v[k].z * w1;
+            a.w = a.w * w0 + v[k].w * w1;
+        }
+    }
+    if (WAYS > 1) {
+        __shared__ float4 sa[256];
+        __shared__ float2 sm[256];
+        sa[threadIdx.x] = a;
+        sm[threadIdx.x] = make_float2(M, L);
+        __syncthreads();
+        if (way != 0)
+            return;
+        for (int k = 1; k < WAYS; ++k) {
+            const float2 o = sm[threadIdx.x + k * LPR];
+            const float4 v = sa[threadIdx.x + k * LPR];
+            if (o.y == 0.f)
+                continue;
+            const float m = fmaxf(M, o.x);
+            const float w0 = exp2f(M - m), w1 = exp2f(o.x - m);
+            M = m;
+            L = L * w0 + o.y * w1;
+            a.x = a.x * w0 + v.x * w1;
+            a.y = a.y * w0 + v.y * w1;
+            a.z = a.z * w0 + v.z * w1;
+            a.w = a.w * w0 + v.w * w1;
+        }
+    }
+    if (!in)
         return;
-    float M = -INFINITY;
-    bool some = false;
-    for (int i = 0; i < p.n_parts; ++i) {
-        const float2 ml = p.part_ml[(size_t)i * p.rows + row];
-        if (ml.y != 0.f) {
-            M = fmaxf(M, ml.x);
-            some = true;
-        }
-    }
-    float L = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    for (int i = 0; i < p.n_parts; ++i) {
-        const size_t at = (size_t)i * p.rows + row;
-        const float2 ml = p.part_ml[at];
-        if (ml.y != 0.f) {
-            const float w = exp2f(ml.x - M);
-            const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + c);
-            L += w * ml.y;
-            a0 += w * v.x;
-            a1 += w * v.y;
-            a2 += w * v.z;
-            a3 += w * v.w;
-        }
-    }
-    const float inv = some ? 1.f / L : 0.f;
+    const float inv = L != 0.f ? 1.f / L : 0.f;
     uint2 v;
-    v.x = pack_bf16x2(a0 * inv, a1 * inv);
-    v.y = pack_bf16x2(a2 * inv, a3 * inv);
+    v.x = pack_bf16x2(a.x * inv, a.y * inv);
+    v.y = pack_bf16x2(a.z * inv, a.w * inv);
     *reinterpret_cast<uint2 *>(p.o + row * D + c) = v;
-    if (c == 0 && p.lse) {
-        const long long bt = row / p.Hq;
-        const int h = (int)(row % p.Hq);
-        const long long b = bt / p.Lq, t = bt % p.Lq;
-        p.lse[(b * p.Hq + h) * p.Lq + t] = some ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-    }
+    if (c == 0 && p.lse)
+        p.lse[(b * p.Hq + h) * p.Lq + t] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// How the work is split: fills the tiling and the split of p.
-static void prefix_plan(PrefixParams &p)
+// How the work is split: fills the tiling and the split of p.  False when the
+// own-key stream does not fit 32-bit arithmetic.
+static bool prefix_plan(PrefixParams &p, int d)
 {
     auto up = [](long long a, long long b) { return (a + b - 1) / b; };
     p.g = p.Hq / p.Hkv;
@@ -645,36 +835,77 @@ static void prefix_plan(PrefixParams &p)
     long long raw = p.W > 0 ? (long long)p.W + span - 1 : 0;
     if (raw > p.Lkv)
         raw = p.Lkv;
-    const long long Tp = up(p.Np, kPfBN), To = up(p.Nc, kPfBN) + up(raw, kPfBN);
+    const long long Tp = up(p.Np, kPfBN);
+    long long To = up(p.Nc, kPfBN) + up(raw, kPfBN);
     const long long Ip = Tp ? (long long)p.p_units * p.Hkv : 0;
     const long long Io = p.Nc > 0 || p.W > 0 ? (long long)p.o_units * p.Hkv * p.B : 0;
-    // Equal chunks of key tiles for w waves of CTAs; of these, the least
-    // waves x (chunk + what an item costs beside its tiles, about three tiles).
-    const long long total = Ip * Tp + Io * To;
-    long long best = -1, chunk = 1;
-    for (long long w = 1; w <= 4; ++w) {
-        long long c = up(total, w * kPfPlanSMs);
-        if (c < 1)
-            c = 1;
-        for (int it = 0; it < 64 && Ip * up(Tp, c) + Io * up(To > 0 ? To : 1, c) > w * kPfPlanSMs; ++it) {
-            if (c >= Tp && c >= To)
-                break;
-            c += up(c, 16);
-        }
-        const long long items = Ip * up(Tp, c) + Io * up(To > 0 ? To : 1, c);
-        const long long longest = c < (Tp > To ? Tp : To) ? c : (Tp > To ? Tp : To);
-        const long long cost = up(items, kPfPlanSMs) * (longest + 3);
+    if (To < 1)
+        To = 1;
+    // Costs in units of 1/8 us, measured: a key tile of a pair, one of an
+    // alternating item, what an item costs beside its tiles.
+    const long long wp = p.p_pair ? kPfPairCost : kPfAltCost, wo = p.o_pair ? kPfPairCost : kPfAltCost, over = kPfItemCost;
+    p.o_over = (int)over;
+    const long long olen = To * wo + over, total_o = Io * olen;
+    if (total_o >= (1LL << 30))
+        return false;
+    p.o_len = (int)olen;
+    // Pieces of the shared entries: the number for which the longest CTA, plus the
+    // traffic of the parts (written and read once, about 4 TB/s), is shortest.
+    const double part = (double)p.rows * (d * 4 + 8) * 2 / 4e6 * 8 * (p.p_pair ? 1 : 2);
+    double best = -1;
+    p.p_ns = Ip ? 1 : 0;
+    for (long long ns = 1; Ip && ns <= Tp && ns <= kPfPlanSMs; ++ns) {
+        const long long piece = up(Tp, ns) * wp + over;
+        const double longest = (double)up(Ip * ns, kPfPlanSMs) * piece;
+        const double mean = (double)(Ip * ns * piece + total_o) / kPfPlanSMs;
+        const double cost = (longest > mean ? longest : mean) + part * ns;
         if (best < 0 || cost < best) {
             best = cost;
-            chunk = c;
+            p.p_ns = (int)ns;
         }
     }
-    p.p_ns = Ip ? (int)up(Tp, chunk) : 0;
-    p.o_ns = Io ? (int)up(To > 0 ? To : 1, chunk) : 0;
+    const long long piece = Ip ? up(Tp, p.p_ns) * wp + over : 0;
+    p.p_pieces = (int)(Ip * p.p_ns);
     p.p_parts = p.p_ns * (p.p_pair ? 1 : 2);
-    p.n_parts = p.p_parts + p.o_ns * (p.o_pair ? 1 : 2);
-    p.n_items_p = (int)(Ip * p.p_ns);
-    p.n_items = (int)(p.n_items_p + Io * p.o_ns);
+    p.ctas = kPfPlanSMs;
+    const long long cnt = p.p_pieces / p.ctas, rem = p.p_pieces % p.ctas;
+    const long long quota = up((long long)p.p_pieces * piece + total_o, p.ctas);
+    const long long least = over + 2 * wo;        // a share worth its overhead
+    long long a = quota - (cnt + 1) * piece, b = quota - cnt * piece;
+    if (rem == 0)
+        a = b;
+    if (a < least) {
+        a = 0;
+        b = up(total_o, p.ctas - rem);
+    }
+    if (b < least)
+        b = least;
+    if (b >= 8 * olen) {     // many items a CTA: whole ones, so that no row has a second part
+        a = up(a, olen) * olen;
+        b = up(b, olen) * olen;
+    }
+    p.o_rem = a > 0 || rem < p.ctas ? (int)rem : 0;
+    p.o_a = (int)a;
+    p.o_b = (int)b;
+    p.o_total = Io ? (int)total_o : 0;
+    // most CTAs that an own item can be spread over
+    long long o_parts = 0;
+    if (Io) {
+        const long long small = a > 0 && a < b ? a : b;
+        o_parts = b % olen == 0 && a % olen == 0 ? 1 : (olen - 2) / small + 2;
+        if (total_o <= small)
+            o_parts = 1;
+        if (o_parts > p.ctas)
+            o_parts = p.ctas;
+        o_parts *= p.o_pair ? 1 : 2;
+    }
+    p.n_parts = p.p_parts + (int)o_parts;
+    // CTAs with something to do
+    int last = p.p_pieces < p.ctas ? p.p_pieces : p.ctas;
+    if (Io && pf_cta(p, p.o_total - 1) + 1 > last)
+        last = pf_cta(p, p.o_total - 1) + 1;
+    p.ctas_used = last;
+    return true;
 }
 
 static size_t prefix_ml_bytes(const PrefixParams &p)
@@ -693,7 +924,8 @@ size_t prefix_workspace_bytes(int B, int Lq, int Lkv, int Hq, int Hkv, int d, in
     p.Np = Np;
     p.Nc = Nc;
     p.W = W;
-    prefix_plan(p);
+    if (!prefix_plan(p, d))
+        return ~(size_t)0;
     return prefix_ml_bytes(p) + (((size_t)p.n_parts * p.rows * d * sizeof(float) + 255) & ~(size_t)255);
 }
 
@@ -705,7 +937,7 @@ static cudaError_t launch_prefix_t(PrefixParams &p, const void *q, const void *k
     using SM = PrefixSmem<D>;
     p.part_ml = static_cast<float2 *>(ws);
     p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + prefix_ml_bytes(p));
-    if (p.n_items > 0) {
+    if (p.ctas_used > 0) {
         // absent tensors: a map that no copy uses
         const bool own = p.Nc > 0, raw = p.W > 0 && p.Lkv > 0;
         CUtensorMap mqp, mqo, mkp, mvp, mkc, mvc, mkr, mvr;
@@ -729,14 +961,18 @@ static cudaError_t launch_prefix_t(PrefixParams &p, const void *q, const void *k
         e = check_reg_split(kern, kPfThreads, 256, kPfSoftmaxRegs, kPfOtherRegs);
         if (e != cudaSuccess)
             return e;
-        const int grid = p.n_items < num_sms ? p.n_items : num_sms;
-        e = launch_pdl(kern, dim3((unsigned)grid), dim3(kPfThreads), ask, stream, mqp, mqo, mkp, mvp, mkc, mvc,
+        e = launch_pdl(kern, dim3((unsigned)p.ctas_used), dim3(kPfThreads), ask, stream, mqp, mqo, mkp, mvp, mkc, mvc,
                        mkr, mvr, p);
         if (e != cudaSuccess)
             return e;
     }
-    const long long blocks = (p.rows * (D / 4) + 255) / 256;
-    return launch_pdl(prefix_combine_kernel<D>, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+    // with eight parts a lane group or more, eight groups share a row
+    constexpr int GROUPS = 256 / (D / 4);
+    if (p.n_parts >= 64)
+        return launch_pdl(prefix_combine_kernel<D, 8>, dim3((unsigned)((p.rows * 8 + GROUPS - 1) / GROUPS)),
+                          dim3(256), 0, stream, p);
+    return launch_pdl(prefix_combine_kernel<D, 1>, dim3((unsigned)((p.rows + GROUPS - 1) / GROUPS)), dim3(256), 0,
+                      stream, p);
 }
 
 cudaError_t launch_prefix_attn(int B, int Lq, int Lkv, int Hq, int Hkv, int d, int Np, int Nc, int m, int W,
@@ -759,7 +995,8 @@ cudaError_t launch_prefix_attn(int B, int Lq, int Lkv, int Hq, int Hkv, int d, i
     p.kv_pos0 = kv_pos0;
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
-    prefix_plan(p);
+    if (!prefix_plan(p, d))
+        return cudaErrorInvalidValue;
     return d == 128 ? launch_prefix_t<128>(p, q, kp, vp, kc, vc, kr, vr, ws, stream, num_sms)
                     : launch_prefix_t<64>(p, q, kp, vp, kc, vc, kr, vr, ws, stream, num_sms);
 }

@@ -97,7 +97,10 @@ hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, cons
         return HYB_ERR_INVALID_ARG;
     if (p->W > 0 && (!k_raw || !v_raw || !aligned16(k_raw) || !aligned16(v_raw)))
         return HYB_ERR_INVALID_ARG;
-    if (!ws_ok(ws, ws_bytes, hyb_prefix_workspace_size(p, Np)))
+    const size_t need = hyb_prefix_workspace_size(p, Np);
+    if (need == ~(size_t)0)
+        return HYB_ERR_UNSUPPORTED;   // more key tiles than the split counts
+    if (!ws_ok(ws, ws_bytes, need))
         return HYB_ERR_WORKSPACE;
     return cuda_status(launch_prefix_attn(p->B, p->Lq, p->Lkv, p->Hq, p->Hkv, p->d, Np, p->Nc, p->m, p->W,
                                           softmax_scale(p), p->q_pos, p->kv_pos0, q, kp, vp, kc, vc, k_raw,
