@@ -22,23 +22,24 @@
 // A query tile holds hpt heads of one KV group x tpt tokens (hpt = min(g, 128),
 // tpt = 128 / hpt), fetched by one TMA box; rows past hpt * tpt are not used.
 //
-// Roles (384 threads):
-//   warps 0-3   softmax + epilogue of query tile (or key stream) A, warps 4-7 of
-//               B: one thread per TMEM lane (= query row).
-//   warp 8      TMA producer (K and V rings of two 32 KB stages each).
-//   warps 9, 10 MMA issue for A and for B.  One thread for both left the tensor
+// Roles (640 threads):
+//   warps 0-7   softmax + epilogue of query tile (or key stream) A, warps 8-15 of
+//               B: two threads per TMEM lane (= query row), one for each half of the
+//               tile's 128 keys; they exchange the row maximum through shared
+//               memory.  A single thread per row issued an instruction every four
+//               to five clocks whatever its work, and with two such warps a
+//               scheduler the softmax took 2200 clocks a tile.
+//   warp 16     TMA producer (K and V rings of two 32 KB stages each).
+//   warps 17, 18 MMA issue for A and for B.  One thread for both left the tensor
 //               pipe idle while it walked from barrier to barrier (a key tile of
 //               a pair took 4650 clocks, 2048 of them MMAs); with a warp each the
 //               two chains only meet in the tensor pipe.  They also zero, in shared memory, the
 //               V rows of a tile that no query of the item sees, so that whatever
 //               such cache rows hold (0 x NaN = NaN) never enters O.  Masked
 //               scores are replaced, not added to, for the same reason.
-//   warp 11     works out the items (the positions of an item's tokens decide how
+//   warp 19     works out the items (the positions of an item's tokens decide how
 //               many keys it has) three ahead, so that no role waits for global
 //               loads between items.
-// The softmax loops over 64-column halves instead of unrolling the tile: short
-// items run through the code once, and its instruction fetches were what they
-// waited for.
 #include "common.cuh"
 
 namespace hyb {
@@ -68,17 +69,19 @@ __device__ __forceinline__ bool elect_one()
     return pred != 0;
 }
 
-constexpr int kPfThreads = 384;
-constexpr int kPfSoftmaxRegs = 208;   // 2 x 128 x 208 + 128 x 88 = 384 x 168 (the launch budget)
-constexpr int kPfOtherRegs = 88;
+constexpr int kPfThreads = 640;
+constexpr int kPfSoftmaxThreads = 512;
+constexpr int kPfSoftmaxRegs = 104;   // 512 x 104 + 128 x 64 = 640 x 96 (the launch budget)
+constexpr int kPfOtherRegs = 64;
 constexpr int kPfBM = 128;
 constexpr int kPfBN = 128;
 constexpr int kPfStages = 2;
 constexpr int kPfItemSlots = 3;
+constexpr int kPfPolyPairs = 2;       // of eight pairs of exponentials
 // The split is planned for this many SMs on every device, so that the workspace
 // size is a function of the problem alone.
 constexpr int kPfPlanSMs = 148;
-constexpr int kPfPairCost = 14, kPfAltCost = 12, kPfItemCost = 20;    // 1/8 us, see prefix_plan
+constexpr int kPfPairCost = 17, kPfAltCost = 8, kPfItemCost = 20;    // 1/8 us, see prefix_plan
 
 struct PrefixParams {
     int B, Lq, Lkv, Hq, Hkv, g, Np, Nc, m, W;
@@ -101,6 +104,28 @@ struct PrefixParams {
     __nv_bfloat16 *o;             // [B, Lq, Hq, D]
     float *lse;                   // [B, Hq, Lq] or NULL
 };
+
+// 2^x for a pair without the exponential unit: x = i + f with i the nearest
+// integer (read off the low bits of x + 1.5 2^23), 2^f by its degree-4 minimax
+// polynomial on [-1/2, 1/2] (fitted by iteratively reweighted least squares;
+// relative error below 2.8e-6, far inside the rounding of P to bf16), i added to the exponent
+// field.  Below -126 (masked scores are -infinity) the result is 0; x <= 8 here.
+__device__ __forceinline__ void exp2_poly2(float x0, float x1, float &e0, float &e1)
+{
+    const uint64_t x = f2(x0, x1);
+    const uint64_t t = add_f2(x, f2(12582912.f, 12582912.f));
+    const uint64_t i = add_f2(t, f2(-12582912.f, -12582912.f));
+    const uint64_t f = fma_f2(i, f2(-1.f, -1.f), x);
+    uint64_t q = fma_f2(f, f2(0.0095701003f, 0.0095701003f), f2(0.055917859f, 0.055917859f));
+    q = fma_f2(q, f, f2(0.24024744f, 0.24024744f));
+    q = fma_f2(q, f, f2(0.69312179f, 0.69312179f));
+    q = fma_f2(q, f, f2(0.99999928f, 0.99999928f));
+    float t0, t1, q0, q1;
+    f2_split(t, t0, t1);
+    f2_split(q, q0, q1);
+    e0 = x0 < -126.f ? 0.f : __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
+    e1 = x1 < -126.f ? 0.f : __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+}
 
 // A work item, as the roles read it from shared memory.
 struct PrefixItem {
@@ -126,12 +151,13 @@ template <int D>
 struct PrefixSmem {
     static constexpr int Q_BYTES = kPfBM * D * 2;
     static constexpr int KV_BYTES = kPfBN * D * 2;
-    static constexpr int STAGE_BYTES = 32 * 64;                        // per softmax warp: 32 rows x 16 channels
+    static constexpr int STAGE_BYTES = 32 * 32;                        // per softmax warp: 32 rows x 8 channels
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = 2 * Q_BYTES;
     static constexpr int OFF_V = OFF_K + kPfStages * KV_BYTES;
     static constexpr int OFF_ST = OFF_V + kPfStages * KV_BYTES;
-    static constexpr int OFF_TOK = OFF_ST + 8 * STAGE_BYTES;
+    static constexpr int OFF_MAX = OFF_ST + 16 * STAGE_BYTES;          // per softmax thread: maximum, then sum
+    static constexpr int OFF_TOK = OFF_MAX + kPfSoftmaxThreads * 4;
     static constexpr int OFF_ITEM = OFF_TOK + kPfItemSlots * 256 * (int)sizeof(PrefixToken);
     static constexpr int OFF_BAR = (OFF_ITEM + kPfItemSlots * (int)sizeof(PrefixItem) + 15) / 16 * 16;
     static constexpr int OFF_MISC = OFF_BAR + 32 * 8;
@@ -283,19 +309,19 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             mbar_init(&bar[PB_VF + s], 1);
             mbar_init(&bar[PB_VE + s], 2);
             mbar_init(&bar[PB_SF + s], 1);
-            mbar_init(&bar[PB_PF + s], 4);     // one arrival a warp
+            mbar_init(&bar[PB_PF + s], 8);     // one arrival a warp
             mbar_init(&bar[PB_OF + s], 1);
-            mbar_init(&bar[PB_OE + s], 4);
+            mbar_init(&bar[PB_OE + s], 8);
         }
         for (int s = 0; s < kPfItemSlots; ++s) {
             mbar_init(&bar[PB_IF + s], 1);
-            mbar_init(&bar[PB_IE + s], 11);    // producer, MMA and softmax warps
+            mbar_init(&bar[PB_IE + s], 19);    // producer, MMA and softmax warps
         }
         mbar_init(&bar[PB_DONE], 2);
         mbar_fence_init();
         misc[1] = 0;
     }
-    if (warp == 9)
+    if (warp == 17)
         tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), 512);
     tc_fence_before();
     __syncthreads();
@@ -321,9 +347,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
     };
 
     constexpr uint32_t TM_O = 2 * kPfBN;         // S_A, S_B, then O_A, O_B (128 columns each)
-    if (warp >= 8)
+    if (warp >= 16)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPfOtherRegs));
-    if (warp == 11) {
+    if (warp == 19) {
         // ================================ items ================================
         uint32_t n = 0;
         bool ok = true;
@@ -357,7 +383,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         }
         if (ok)
             next(false, -1, 0, 0, 0);
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ================================ producer ================================
         const uint32_t q_bytes = (uint32_t)p.hpt * p.tpt * D * 2;
         uint32_t kc = 0, vc = 0, nq = 0, qn = 0;
@@ -426,9 +452,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             for (uint32_t c = (vc > kPfStages ? vc - kPfStages : 0); c < vc; ++c)
                 drain_wait(&bar[PB_VF + c % kPfStages], (c / kPfStages) & 1);
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 16) {
         // ================================ MMA issue ================================
-        const int x = warp - 9;
+        const int x = warp - 17;
         const uint32_t idesc_qk = idesc_bf16(kPfBM, kPfBN, false, false);
         const uint32_t idesc_pv = idesc_bf16(kPfBM, D, false, true);
         const uint32_t aK = smem_u32(sK), aV = smem_u32(sV);
@@ -477,7 +503,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
 #pragma unroll
                         for (int kk = 0; kk < kPfBN / 16; ++kk) {
                             const uint64_t db = sw128_desc(aV + vs * SM::KV_BYTES + kk * 16 * 128, kPfBN * 128, 1024);
-                            mma_bf16_ts(tO, tS + kk * 8, db, idesc_pv, (t == first + step && kk == 0) ? 0u : 1u);
+                            // P of keys 64 .. 127 starts at column 64
+                            mma_bf16_ts(tO, tS + (kk >> 2) * 64 + (kk & 3) * 8, db, idesc_pv,
+                                        (t == first + step && kk == 0) ? 0u : 1u);
                         }
                         mma_commit(&bar[PB_VE + vs]);
                         if (alone)
@@ -522,16 +550,22 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPfSoftmaxRegs));
         // ========================== softmax + epilogue ==========================
-        const int x = warp >> 2;            // 0: A, 1: B
+        const int x = warp >> 3;            // 0: A, 1: B
+        const int half = (warp >> 2) & 1;   // keys 64 half .. of a tile, channels D / 2 half .. of O
         const int quad = warp & 3;
         const int row = quad * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t tS = tl + x * kPfBN;
-        const uint32_t tO = tl + TM_O + x * 128;
+        const uint32_t tS = tl + x * kPfBN + half * 64;
+        const uint32_t tO = tl + TM_O + x * 128 + half * (D / 2);
+        float *mine = reinterpret_cast<float *>(smem + SM::OFF_MAX) + threadIdx.x;
+        const float *other = reinterpret_cast<float *>(smem + SM::OFF_MAX) + (threadIdx.x ^ 128);
+        // the two warps of a row quad meet (barriers 1 .. 8)
+        auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + quad) : "memory"); };
         uint8_t *stage = smem + SM::OFF_ST + warp * SM::STAGE_BYTES;
         const int rtok = row / p.hpt, rhead = row % p.hpt;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
         uint32_t scnt = 0, ocnt = 0, nq = 0;
+        uint32_t theirs = 0;                // tiles of the other warpgroups so far
         bool ok = true;
         PrefixItem it;
         while (ok && item(nq, it)) {
@@ -545,6 +579,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 tk = sTok[(nq % kPfItemSlots) * 256 + xt * 128 + rtok];
             release(nq);
             const bool warp_rows = __any_sync(0xffffffffu, valid_row);
+            const bool turns = it.pair && it.val1;
             const int flat = (it.pre ? 0 : it.b * p.Lq) + tok;
             float m_ref = -INFINITY, l_sum = 0.f;
             for (int t = first; t < it.nt; t += step) {
@@ -553,46 +588,49 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 ++scnt;
                 tc_fence_after();
                 if (warp_rows) {
-                    // columns c_lo .. c_lo + c_n of this key tile are visible to this row
+                    // keys c_lo .. c_lo + c_n of this half of the tile are visible to this row
                     int c_lo = 0, c_hi;
                     const int kt = it.t0 + t;
                     if (kt < it.nte) {
-                        c_hi = min(tk.nv - 1 - kt * kPfBN, kPfBN - 1);
+                        c_hi = min(tk.nv - 1 - kt * kPfBN - half * 64, 63);
                     } else {
-                        const int r0 = it.rlo + (kt - it.nte) * kPfBN;
+                        const int r0 = it.rlo + (kt - it.nte) * kPfBN + half * 64;
                         c_lo = max(0, tk.wlo - r0);
-                        c_hi = min(tk.whi - r0, kPfBN - 1);
+                        c_hi = min(tk.whi - r0, 63);
                     }
-                    const bool full = __all_sync(0xffffffffu, c_lo == 0 && c_hi == kPfBN - 1);
+                    // (rows of no query go along with the others: nothing of theirs is kept)
+                    const bool full = __all_sync(0xffffffffu, !valid_row || (c_lo == 0 && c_hi == 63));
                     if (c_hi < c_lo) {
                         c_lo = 1 << 20;
                         c_hi = c_lo;
                     }
                     const unsigned c_n = (unsigned)(c_hi - c_lo);
-                    // row maximum
-                    float tmax = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < kPfBN; c += 64) {
-                        float sv[64];
-                        tmem_ld32(tS + c, *reinterpret_cast<float(*)[32]>(&sv[0]));
-                        tmem_ld32(tS + c + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
-                        tmem_ld_wait();
-                        if (!full) {
+                    float v[64];
+                    tmem_ld32(tS, *reinterpret_cast<float(*)[32]>(&v[0]));
+                    tmem_ld32(tS + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
+                    tmem_ld_wait();
+                    if (!full) {
 #pragma unroll
-                            for (int q = 0; q < 64; ++q)
-                                sv[q] = (unsigned)(c + q - c_lo) <= c_n ? sv[q] : -INFINITY;
-                        }
+                        for (int q = 0; q < 64; ++q)
+                            v[q] = (unsigned)(q - c_lo) <= c_n ? v[q] : -INFINITY;
+                    }
+                    // row maximum
+                    float tmax;
+                    {
                         float mk[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            float a = fmax3f(sv[16 * k], sv[16 * k + 1], sv[16 * k + 2]);
+                            float a = fmax3f(v[16 * k], v[16 * k + 1], v[16 * k + 2]);
 #pragma unroll
                             for (int q = 3; q < 15; q += 2)
-                                a = fmax3f(a, sv[16 * k + q], sv[16 * k + q + 1]);
-                            mk[k] = fmaxf(a, sv[16 * k + 15]);
+                                a = fmax3f(a, v[16 * k + q], v[16 * k + q + 1]);
+                            mk[k] = fmaxf(a, v[16 * k + 15]);
                         }
-                        tmax = fmax3f(tmax, fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
+                        tmax = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
                     }
+                    *mine = tmax;
+                    meet();
+                    tmax = fmaxf(tmax, *other);
                     tmax *= p.scale_log2;  // the scale is positive
                     // the reference maximum moves (and O is rescaled) only when a
                     // tile raises it by more than 2^8
@@ -605,48 +643,51 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                     if (t > first && __any_sync(0xffffffffu, alpha != 1.f)) {
                         // O holds every earlier PV (S_full covers all MMAs issued before this QK)
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float ov[32];
-                            tmem_ld32(tO + c, ov);
+                        for (int c = 0; c < D / 2; c += 8) {
+                            float ov[8];
+                            tmem_ld8(tO + c, ov);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int q = 0; q < 32; ++q)
+                            for (int q = 0; q < 8; ++q)
                                 ov[q] *= alpha;
-                            tmem_st32(tO + c, ov);
+                            tmem_st8(tO + c, ov);
                         }
                     }
+                    // Turns: B's exponentials of a tile follow A's, and A's next ones follow
+                    // B's, so that one query tile's run under the other's MMAs.  (Left
+                    // alone the two fall into step: both exponentiate, then both wait.)
+                    if (turns && (x || t > 0) &&
+                        !(ok = wait(PB_PF + (x ^ 1), (x ? theirs + t : theirs + t - 1) & 1)))
+                        break;
                     // P = exp2(s * scale - mu), rounded to bf16 (the MMA operand; its
                     // relative error 2^-8 a term averages out below the output's own
-                    // rounding) over the first 64 columns of S; the row sum is of the
-                    // fp32 values.  Half 0's P lies over columns 0-31, which are read.
+                    // rounding) over the first half of this thread's columns of S; the
+                    // row sum is of the fp32 values.
+                    // Some of the exponentials are polynomials: the unit's 16 a clock
+                    // are what a pair's softmax would wait for.
                     const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
                     const uint64_t nmu2 = f2(-mu, -mu);
                     uint64_t lacc[2] = {0ull, 0ull};
-#pragma unroll 1
-                    for (int c = 0; c < kPfBN; c += 64) {
-                        float sv[64];
-                        tmem_ld32(tS + c, *reinterpret_cast<float(*)[32]>(&sv[0]));
-                        tmem_ld32(tS + c + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
-                        tmem_ld_wait();
-                        if (!full) {
 #pragma unroll
-                            for (int q = 0; q < 64; ++q)
-                                sv[q] = (unsigned)(c + q - c_lo) <= c_n ? sv[q] : -INFINITY;
-                        }
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t pk[16];
 #pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int q = 0; q < 32; q += 2) {
-                                float x0, x1;
-                                f2_split(fma_f2(f2(sv[hh * 32 + q], sv[hh * 32 + q + 1]), sc2, nmu2), x0, x1);
-                                const float e0 = ex2_approx(x0);
-                                const float e1 = ex2_approx(x1);
-                                lacc[(q >> 1) & 1] = add_f2(lacc[(q >> 1) & 1], f2(e0, e1));
-                                pk[q >> 1] = pack_bf16x2(e0, e1);
+                        for (int q = c; q < c + 32; q += 2) {
+                            float x0, x1;
+                            f2_split(fma_f2(f2(v[q], v[q + 1]), sc2, nmu2), x0, x1);
+                            if ((q >> 1) % 8 < kPfPolyPairs) {
+                                float e0, e1;
+                                exp2_poly2(x0, x1, e0, e1);
+                                x0 = e0;
+                                x1 = e1;
+                            } else {
+                                x0 = ex2_approx(x0);
+                                x1 = ex2_approx(x1);
                             }
-                            tmem_st16(tS + (c >> 1) + hh * 16, pk);
+                            lacc[(q >> 1) & 1] = add_f2(lacc[(q >> 1) & 1], f2(x0, x1));
+                            pk[(q - c) >> 1] = pack_bf16x2(x0, x1);
                         }
+                        tmem_st16(tS + (c >> 1), pk);
                     }
                     float a0, a1;
                     f2_split(add_f2(lacc[0], lacc[1]), a0, a1);
@@ -667,47 +708,76 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 ++ocnt;
                 tc_fence_after();
             }
+            if (warp_rows) {
+                *mine = l_sum;
+                meet();
+                l_sum += *other;
+                meet();          // before the next item's first maximum
+            }
             const long long at = (long long)(it.part + (it.pair ? 0 : x)) * p.rows + (long long)flat * p.Hq + h;
-            if (valid_row)
+            if (valid_row && half == 0)
                 p.part_ml[at] = make_float2(m_ref, l_sum);
             const unsigned stored = __ballot_sync(0xffffffffu, valid_row && l_sum != 0.f);
             if (stored) {
-                // sixteen channels of the warp's rows at a time, through shared
-                // memory, so that a store instruction writes 64 bytes of eight rows
-                float *orow = p.part_o + at * D;
+                float *orow = p.part_o + at * D + half * (D / 2);
+                if (__popc(stored) <= 8) {
+                    // few rows: each lane writes its own
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float ov[16];
-                    tmem_ld16(tO + c, ov);
-                    tmem_ld_wait();
+                    for (int c = 0; c < D / 2; c += 32) {
+                        float ov[32];
+                        tmem_ld32(tO + c, ov);
+                        tmem_ld_wait();
+                        if ((stored >> lane) & 1) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<float4 *>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-                            make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
-                    __syncwarp();
-#pragma unroll
-                    for (int r8 = 0; r8 < 32; r8 += 8) {
-                        const int r = r8 + (lane >> 2), q = lane & 3;
-                        float *dst = reinterpret_cast<float *>(
-                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(orow), r));
-                        if ((stored >> r) & 1)
-                            *reinterpret_cast<float4 *>(dst + c + 4 * q) =
-                                *reinterpret_cast<const float4 *>(stage + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+                            for (int q = 0; q < 32; q += 4)
+                                *reinterpret_cast<float4 *>(orow + c + q) =
+                                    make_float4(ov[q], ov[q + 1], ov[q + 2], ov[q + 3]);
+                        }
                     }
-                    __syncwarp();
+                } else {
+                    // eight channels of the warp's rows at a time, through shared memory,
+                    // so that a store instruction writes whole 32-byte sectors
+                    const int r = lane >> 1, q = lane & 1;
+                    float *dst[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        dst[k] = reinterpret_cast<float *>(__shfl_sync(
+                                     0xffffffffu, reinterpret_cast<unsigned long long>(orow), r + 16 * k)) + 4 * q;
+                    const uint8_t *src = stage + r * 32 + ((q ^ ((r >> 2) & 1)) << 4);
+                    uint8_t *put = stage + lane * 32 + (((lane >> 2) & 1) << 4);
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; c += 32) {
+                        float ov[32];
+                        tmem_ld32(tO + c, ov);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            *reinterpret_cast<float4 *>(put) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                            *reinterpret_cast<float4 *>(stage + ((put - stage) ^ 16)) =
+                                make_float4(ov[e + 4], ov[e + 5], ov[e + 6], ov[e + 7]);
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                if ((stored >> (r + 16 * k)) & 1)
+                                    *reinterpret_cast<float4 *>(dst[k] + c + e) =
+                                        *reinterpret_cast<const float4 *>(src + k * 512);
+                            __syncwarp();
+                        }
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0 && first < it.nt)
                 mbar_arrive(&bar[PB_OE + x]);
+            theirs += turns ? it.nt : it.pair ? (x ? it.nt : 0) : (it.nt + x) / 2;
             ++nq;
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc((uint32_t)misc[0], 512);
     }
@@ -851,35 +921,56 @@ static bool prefix_plan(PrefixParams &p, int d)
     p.o_len = (int)olen;
     // Pieces of the shared entries: the number for which the longest CTA, plus the
     // traffic of the parts (written and read once, about 4 TB/s), is shortest.
+    // Own keys fill up the CTAs with fewer pieces, or all of them evenly: shares a
+    // (CTAs with one piece more) and b; a share that cuts an item pays `over` again.
     const double part = (double)p.rows * (d * 4 + 8) * 2 / 4e6 * 8 * (p.p_pair ? 1 : 2);
+    const long long least = over + wo;            // a share worth its overhead
     double best = -1;
-    p.p_ns = Ip ? 1 : 0;
-    for (long long ns = 1; Ip && ns <= Tp && ns <= kPfPlanSMs; ++ns) {
-        const long long piece = up(Tp, ns) * wp + over;
-        const double longest = (double)up(Ip * ns, kPfPlanSMs) * piece;
-        const double mean = (double)(Ip * ns * piece + total_o) / kPfPlanSMs;
-        const double cost = (longest > mean ? longest : mean) + part * ns;
-        if (best < 0 || cost < best) {
-            best = cost;
-            p.p_ns = (int)ns;
+    long long a = 0, b = least, cnt = 0, rem = 0;
+    p.ctas = kPfPlanSMs;
+    for (long long len = Ip ? Tp : 1, ns_last = 0; len >= 1; len -= 1 + len / 8) {
+        const long long ns = Ip ? up(Tp, len) : 0;
+        if (ns > kPfPlanSMs)
+            break;
+        if (Ip && ns == ns_last)
+            continue;
+        ns_last = ns;
+        const long long piece = Ip ? up(Tp, ns) * wp + over : 0, pieces = Ip * ns;
+        const long long n = pieces / p.ctas, r = pieces % p.ctas;
+        const long long quota = up(pieces * piece + total_o, p.ctas);
+        for (int even = 0; even < 2; ++even) {
+            long long sa = quota - (n + 1) * piece, sb = quota - n * piece;
+            if (r == 0)
+                sa = sb;
+            if (even || sa < least) {
+                sa = 0;
+                sb = up(total_o, p.ctas - r);
+            }
+            if (sb < least)
+                sb = least;
+            const long long cut = total_o && sb < 8 * olen ? over : 0;
+            long long longest = n * piece + (total_o ? sb : 0) + cut;
+            const long long other = (r ? (n + 1) * piece + sa + (sa ? cut : 0) : 0);
+            if (other > longest)
+                longest = other;
+            const double cost = (double)longest + part * ns;
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.p_ns = (int)ns;
+                cnt = n;
+                rem = r;
+                a = sa;
+                b = sb;
+            }
+            if (!total_o)
+                break;
         }
+        if (!Ip)
+            break;
     }
-    const long long piece = Ip ? up(Tp, p.p_ns) * wp + over : 0;
+    (void)cnt;
     p.p_pieces = (int)(Ip * p.p_ns);
     p.p_parts = p.p_ns * (p.p_pair ? 1 : 2);
-    p.ctas = kPfPlanSMs;
-    const long long cnt = p.p_pieces / p.ctas, rem = p.p_pieces % p.ctas;
-    const long long quota = up((long long)p.p_pieces * piece + total_o, p.ctas);
-    const long long least = over + 2 * wo;        // a share worth its overhead
-    long long a = quota - (cnt + 1) * piece, b = quota - cnt * piece;
-    if (rem == 0)
-        a = b;
-    if (a < least) {
-        a = 0;
-        b = up(total_o, p.ctas - rem);
-    }
-    if (b < least)
-        b = least;
     if (b >= 8 * olen) {     // many items a CTA: whole ones, so that no row has a second part
         a = up(a, olen) * olen;
         b = up(b, olen) * olen;
@@ -958,7 +1049,7 @@ static cudaError_t launch_prefix_t(PrefixParams &p, const void *q, const void *k
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
         if (e != cudaSuccess)
             return e;
-        e = check_reg_split(kern, kPfThreads, 256, kPfSoftmaxRegs, kPfOtherRegs);
+        e = check_reg_split(kern, kPfThreads, kPfSoftmaxThreads, kPfSoftmaxRegs, kPfOtherRegs);
         if (e != cudaSuccess)
             return e;
         e = launch_pdl(kern, dim3((unsigned)p.ctas_used), dim3(kPfThreads), ask, stream, mqp, mqo, mkp, mvp, mkc, mvc,
