@@ -399,16 +399,17 @@ def hyb_gated_fwd(p: HybProblem, q, kc, vc, idx, k_raw, v_raw, gate, o=None, ws=
 
 # ------------------------------------------------- shared and bounded caches
 def _want(name: str, t: Optional[torch.Tensor], shape, dtype, device, needed: bool = True):
-    """ValueError unless t is a contiguous tensor of this shape, type and device
-    (None only where it is not needed)."""
+    """Address of t after checking that it is a contiguous tensor of this shape,
+    type and device (ValueError otherwise); None only where it is not needed."""
     if t is None:
         if needed:
             raise ValueError(f"{name} is missing")
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}"
                          + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
 
 
 def _want_positions(p: HybProblem, device):
@@ -417,34 +418,39 @@ def _want_positions(p: HybProblem, device):
     _want("kv_pos0", kv_pos0, (p.B,), torch.int32, device, needed=False)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
-    """Makes a tensor's device the current one for a call, and names its stream
-    (the one given, else the device's current stream)."""
+    """A call on a tensor's device (made the current one where it is not) and on
+    the stream given, else the device's current stream."""
+
+    __slots__ = ("device", "stream", "handle", "guard")
 
     def __init__(self, t: torch.Tensor, stream):
-        if t.device.type != "cuda":
+        if not t.is_cuda:
             raise ValueError("the library takes CUDA tensors")
-        self.device = torch.cuda.device(t.device)
-        self.stream = stream if stream is not None else torch.cuda.current_stream(t.device)
-        self.other = stream is not None and stream != torch.cuda.current_stream(t.device)
+        self.device, self.stream = t.device, stream
+        index = t.device.index
+        self.handle = _raw_stream(index) if stream is None else stream.cuda_stream
+        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
     def new(self, shape, dtype):
         """A tensor for this call; the allocator keeps it until the stream is done with it."""
-        t = torch.empty(shape, dtype=dtype, device=self.stream.device)
-        if self.other:
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.stream is not None:
             t.record_stream(self.stream)
         return t
 
     def __enter__(self):
-        self.device.__enter__()
+        if self.guard is not None:
+            self.guard.__enter__()
         return self
 
     def __exit__(self, *exc):
-        self.device.__exit__(*exc)
-
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def hyb_prefix_workspace_size(p: HybProblem, Np: int) -> int:
@@ -456,25 +462,27 @@ def hyb_prefix_attn_fwd(p: HybProblem, q, kp, vp, kc=None, vc=None, k_raw=None, 
     """One softmax over the entries kp / vp [Np, Hkv, d] that every sequence
     shares, the sequence's own entries kc / vc [B, Nc, Hkv, d] (entry Np + j is
     row j) and its raw window.  Returns o [B, Lq, Hq, d] bf16; lse [B, Hq, Lq]
-    fp32 is filled when given."""
-    bf, Np = torch.bfloat16, 0 if kp is None else kp.shape[0]
-    _want("q", q, (p.B, p.Lq, p.Hq, p.d), bf, q.device)
-    for name, t, shape, n in (("kp", kp, (Np,), Np), ("vp", vp, (Np,), Np), ("kc", kc, (p.B, p.Nc), p.Nc),
-                              ("vc", vc, (p.B, p.Nc), p.Nc), ("k_raw", k_raw, (p.B, p.Lkv), p.W),
-                              ("v_raw", v_raw, (p.B, p.Lkv), p.W)):
-        _want(name, t, (*shape, p.Hkv, p.d), bf, q.device, needed=n > 0)
-    _want_positions(p, q.device)
+    fp32 is filled when given.  ws: hyb_prefix_workspace_size(p, Np) bytes,
+    allocated when absent."""
+    bf, dev, Np = torch.bfloat16, q.device, 0 if kp is None else kp.shape[0]
+    B, Hkv, d, Nc, Lkv, W = p.B, p.Hkv, p.d, p.Nc, p.Lkv, p.W
+    rows = (B, p.Lq, p.Hq, d)
+    at = [_want("q", q, rows, bf, dev),
+          _want("kp", kp, (Np, Hkv, d), bf, dev, Np > 0), _want("vp", vp, (Np, Hkv, d), bf, dev, Np > 0),
+          _want("kc", kc, (B, Nc, Hkv, d), bf, dev, Nc > 0), _want("vc", vc, (B, Nc, Hkv, d), bf, dev, Nc > 0),
+          _want("k_raw", k_raw, (B, Lkv, Hkv, d), bf, dev, W > 0),
+          _want("v_raw", v_raw, (B, Lkv, Hkv, d), bf, dev, W > 0)]
+    _want_positions(p, dev)
     with _On(q, stream) as on:
         if o is None:
-            o = on.new((p.B, p.Lq, p.Hq, p.d), bf)
-        _want("o", o, (p.B, p.Lq, p.Hq, p.d), bf, q.device)
-        _want("lse", lse, (p.B, p.Hq, p.Lq), torch.float32, q.device, needed=False)
-        need = hyb_prefix_workspace_size(p, Np)
-        if ws is None or ws.numel() * ws.element_size() < need:
-            ws = on.new((max(need, 256),), torch.uint8)
-        st = _lib.hyb_prefix_attn_fwd(ctypes.byref(p), Np, _ptr(q), _ptr(kp), _ptr(vp), _ptr(kc), _ptr(vc),
-                                      _ptr(k_raw), _ptr(v_raw), _ptr(o), _ptr(lse), _ptr(ws),
-                                      ws.numel() * ws.element_size(), on.handle)
+            o = on.new(rows, bf)
+        at += [_want("o", o, rows, bf, dev), _want("lse", lse, (B, p.Hq, p.Lq), torch.float32, dev, False)]
+        if ws is None:
+            ws = on.new((max(hyb_prefix_workspace_size(p, Np), 256),), torch.uint8)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: expected a contiguous tensor on {dev}")
+        st = _lib.hyb_prefix_attn_fwd(ctypes.byref(p), Np, *at, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                      on.handle)
     _check(st, "hyb_prefix_attn_fwd")
     return o
 
@@ -486,16 +494,16 @@ def hyb_attn_weights(p: HybProblem, q, kc, lse, idx=None, acc=None, accumulate: 
     over the entries idx [B, 1, topk] lists when given.  Added to acc [B, Nc]
     fp32 (accumulate=False: written, 0 for unseen entries); a new tensor when
     acc is None.  e0: entry index of kc's row 0.  Returns acc."""
-    _want("q", q, (p.B, p.Lq, p.Hq, p.d), torch.bfloat16, q.device)
-    _want("kc", kc, (p.B, p.Nc, p.Hkv, p.d), torch.bfloat16, q.device)
-    _want("lse", lse, (p.B, p.Hq, p.Lq), torch.float32, q.device)
-    _want("idx", idx, (p.B, p.Lq, p.topk), torch.int32, q.device, needed=p.topk > 0)
-    _want("acc", acc, (p.B, p.Nc), torch.float32, q.device, needed=False)
-    _want_positions(p, q.device)
+    dev, f32 = q.device, torch.float32
+    at = [_want("q", q, (p.B, p.Lq, p.Hq, p.d), torch.bfloat16, dev),
+          _want("kc", kc, (p.B, p.Nc, p.Hkv, p.d), torch.bfloat16, dev),
+          _want("lse", lse, (p.B, p.Hq, p.Lq), f32, dev),
+          _want("idx", idx, (p.B, p.Lq, p.topk), torch.int32, dev, p.topk > 0)]
+    _want_positions(p, dev)
     with _On(q, stream) as on:
         if acc is None:
-            acc, accumulate = on.new((p.B, p.Nc), torch.float32), False
-        st = _lib.hyb_attn_weights(ctypes.byref(p), _ptr(q), _ptr(kc), _ptr(lse), _ptr(idx), int(e0), _ptr(acc),
+            acc, accumulate = on.new((p.B, p.Nc), f32), False
+        st = _lib.hyb_attn_weights(ctypes.byref(p), *at, int(e0), _want("acc", acc, (p.B, p.Nc), f32, dev),
                                    int(bool(accumulate)), on.handle)
     _check(st, "hyb_attn_weights")
     return acc
@@ -506,39 +514,46 @@ def hyb_evict_select(acc, n_keep: int, n_first: int = 0, n_last: int = 0, n_vali
     the first n_first, the last n_last and the heaviest of the rest by
     acc [B, Nc] fp32, of the n_valid [B] int32 entries it holds (None: all)."""
     B, Nc = acc.shape
-    _want("acc", acc, (B, Nc), torch.float32, acc.device)
-    _want("n_valid", n_valid, (B,), torch.int32, acc.device, needed=False)
+    dev, i32 = acc.device, torch.int32
+    at, nv = _want("acc", acc, (B, Nc), torch.float32, dev), _want("n_valid", n_valid, (B,), i32, dev, False)
     with _On(acc, stream) as on:
         if keep is None:
-            keep = on.new((B, n_keep), torch.int32)
-        _want("keep", keep, (B, n_keep), torch.int32, acc.device)
-        st = _lib.hyb_evict_select(_ptr(acc), B, Nc, _ptr(n_valid), int(n_keep), int(n_first), int(n_last),
-                                   _ptr(keep), on.handle)
+            keep = on.new((B, n_keep), i32)
+        st = _lib.hyb_evict_select(at, B, Nc, nv, int(n_keep), int(n_first), int(n_last),
+                                   _want("keep", keep, (B, n_keep), i32, dev), on.handle)
     _check(st, "hyb_evict_select")
     return keep
 
 
-def _compact_pairs(p, keep, No, on, parts):
-    """(source, output) of every tensor of a compaction; parts: (name, source,
-    output, row shape, dtype), outputs allocated when absent."""
-    out = []
-    for name, x, y, row, dtype in parts:
-        _want(name, x, (p.B, p.Nc, *row), dtype, keep.device, needed=False)
-        if x is not None and y is None:
-            y = on.new((p.B, No, *row), dtype)
-        if x is None and y is not None:
-            raise ValueError(f"{name}_out given without {name}")
-        _want(name + "_out", y, (p.B, No, *row), dtype, keep.device, needed=False)
-        out.append((x, y))
-    return out
-
-
-def _compact_rows(p, keep, outs):
-    """Rows per sequence of the outputs: those of the tensors given, else n_keep."""
+def _compact(fn, p, keep, parts, stream):
+    """One compaction call.  parts: (name, source, output, row shape, dtype) in the
+    order of the C arguments; absent outputs are allocated.  Returns the outputs."""
     if keep.dim() != 2:
         raise ValueError("keep: expected [B, n_keep]")
-    _want("keep", keep, (p.B, keep.shape[1]), torch.int32, keep.device)
-    return next((y.shape[1] for y in outs if y is not None), keep.shape[1])
+    B, Nc, n_keep, dev = p.B, p.Nc, keep.shape[1], keep.device
+    at = _want("keep", keep, (B, n_keep), torch.int32, dev)
+    No = n_keep
+    for _, _, y, _, _ in parts:
+        if y is not None:
+            No = y.shape[1]
+            break
+    src, dst, outs = [], [], []
+    with _On(keep, stream) as on:
+        for name, x, y, row, dtype in parts:
+            if x is None:
+                if y is not None:
+                    raise ValueError(f"{name}_out given without {name}")
+                src.append(None)
+                dst.append(None)
+            else:
+                if y is None:
+                    y = on.new((B, No, *row), dtype)
+                src.append(_want(name, x, (B, Nc, *row), dtype, dev))
+                dst.append(_want(name + "_out", y, (B, No, *row), dtype, dev))
+            outs.append(y)
+        st = fn(ctypes.byref(p), at, n_keep, No, *src, *dst, on.handle)
+    _check(st, fn.__name__)
+    return outs
 
 
 def hyb_cache_compact(p: HybProblem, keep, kc=None, vc=None, kic=None, acc=None, kc_out=None, vc_out=None,
@@ -548,16 +563,11 @@ def hyb_cache_compact(p: HybProblem, keep, kc=None, vc=None, kic=None, acc=None,
     optional, into outputs of No >= n_keep rows per sequence (new tensors of
     n_keep rows when absent; their rows without an entry are not initialised).
     Returns dict(kc, vc, kic, acc) of the outputs."""
-    bf = torch.bfloat16
-    No = _compact_rows(p, keep, (kc_out, vc_out, kic_out, acc_out))
-    with _On(keep, stream) as on:
-        pairs = _compact_pairs(p, keep, No, on, (
-            ("kc", kc, kc_out, (p.Hkv, p.d), bf), ("vc", vc, vc_out, (p.Hkv, p.d), bf),
-            ("kic", kic, kic_out, (p.di,), bf), ("acc", acc, acc_out, (), torch.float32)))
-        st = _lib.hyb_cache_compact(ctypes.byref(p), _ptr(keep), keep.shape[1], No, *(_ptr(x) for x, _ in pairs),
-                                    *(_ptr(y) for _, y in pairs), on.handle)
-    _check(st, "hyb_cache_compact")
-    return dict(zip(("kc", "vc", "kic", "acc"), (y for _, y in pairs)))
+    bf, kv = torch.bfloat16, (p.Hkv, p.d)
+    outs = _compact(_lib.hyb_cache_compact, p, keep,
+                    (("kc", kc, kc_out, kv, bf), ("vc", vc, vc_out, kv, bf), ("kic", kic, kic_out, (p.di,), bf),
+                     ("acc", acc, acc_out, (), torch.float32)), stream)
+    return dict(kc=outs[0], vc=outs[1], kic=outs[2], acc=outs[3])
 
 
 def hyb_cache_compact_fp4(p: HybProblem, keep, kc: Optional[Fp4Cache] = None, vc: Optional[Fp4Cache] = None,
@@ -565,22 +575,15 @@ def hyb_cache_compact_fp4(p: HybProblem, keep, kc: Optional[Fp4Cache] = None, vc
                           vc_out: Optional[Fp4Cache] = None, kic_out: Optional[Fp4Cache] = None, acc_out=None,
                           stream=None):
     """hyb_cache_compact over 4-bit caches."""
-    both = lambda c: (None, None) if c is None else (c.codes, c.qp)
-    No = _compact_rows(p, keep, (*both(kc_out), *both(vc_out), *both(kic_out), acc_out))
-    with _On(keep, stream) as on:
-        parts = []
-        for name, c, o, row, dx in (("kc", kc, kc_out, (p.Hkv,), p.d), ("vc", vc, vc_out, (p.Hkv,), p.d),
-                                    ("kic", kic, kic_out, (), p.di)):
-            (x, xq), (y, yq) = both(c), both(o)
-            parts += [(name, x, y, (*row, dx // 2), torch.uint8), (name + " pairs", xq, yq, (*row, 2), torch.float32)]
-        pairs = _compact_pairs(p, keep, No, on, (*parts, ("acc", acc, acc_out, (), torch.float32)))
-        st = _lib.hyb_cache_compact_fp4(ctypes.byref(p), _ptr(keep), keep.shape[1], No,
-                                        *(_ptr(x) for x, _ in pairs), *(_ptr(y) for _, y in pairs), on.handle)
-    _check(st, "hyb_cache_compact_fp4")
-    out = [y for _, y in pairs]
-    got = {n: None if out[2 * i] is None else Fp4Cache(out[2 * i], out[2 * i + 1])
-           for i, n in enumerate(("kc", "vc", "kic"))}
-    return dict(got, acc=out[6])
+    parts = []
+    for name, c, o, row, dx in (("kc", kc, kc_out, (p.Hkv,), p.d), ("vc", vc, vc_out, (p.Hkv,), p.d),
+                                ("kic", kic, kic_out, (), p.di)):
+        x, xq = (c.codes, c.qp) if c is not None else (None, None)
+        y, yq = (o.codes, o.qp) if o is not None else (None, None)
+        parts += [(name, x, y, (*row, dx // 2), torch.uint8), (name + " pairs", xq, yq, (*row, 2), torch.float32)]
+    out = _compact(_lib.hyb_cache_compact_fp4, p, keep, (*parts, ("acc", acc, acc_out, (), torch.float32)), stream)
+    got = [None if out[2 * i] is None else Fp4Cache(out[2 * i], out[2 * i + 1]) for i in range(3)]
+    return dict(kc=got[0], vc=got[1], kic=got[2], acc=out[6])
 
 
 def hyb_get_device_status(stream=None) -> int:

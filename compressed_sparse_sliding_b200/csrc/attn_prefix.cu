@@ -40,6 +40,8 @@
 //   warp 19     works out the items (the positions of an item's tokens decide how
 //               many keys it has) three ahead, so that no role waits for global
 //               loads between items.
+#include <atomic>
+
 #include "common.cuh"
 
 namespace hyb {
@@ -1004,56 +1006,75 @@ static size_t prefix_ml_bytes(const PrefixParams &p)
     return ((size_t)p.n_parts * p.rows * sizeof(float2) + 255) & ~(size_t)255;
 }
 
-size_t prefix_workspace_bytes(int B, int Lq, int Lkv, int Hq, int Hkv, int d, int Np, int Nc, int W)
+static std::atomic<unsigned long long> g_prefix_ready[2];     // devices, by head dim
+
+static size_t prefix_workspace(const PrefixParams &p, int d)
 {
-    PrefixParams p = {};
-    p.B = B;
-    p.Lq = Lq;
-    p.Lkv = Lkv;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.Np = Np;
-    p.Nc = Nc;
-    p.W = W;
-    if (!prefix_plan(p, d))
-        return ~(size_t)0;
     return prefix_ml_bytes(p) + (((size_t)p.n_parts * p.rows * d * sizeof(float) + 255) & ~(size_t)255);
+}
+
+// The checks and settings of a kernel that hold for the life of the process,
+// made once per device (a function attribute call costs about a microsecond).
+static bool prefix_set_up(int device, int d)
+{
+    return device >= 0 && device < 64 && ((g_prefix_ready[d == 128].load(std::memory_order_acquire) >> device) & 1);
 }
 
 template <int D>
 static cudaError_t launch_prefix_t(PrefixParams &p, const void *q, const void *kp, const void *vp,
                                    const void *kc, const void *vc, const void *kr, const void *vr, void *ws,
-                                   cudaStream_t stream, int num_sms)
+                                   cudaStream_t stream)
 {
     using SM = PrefixSmem<D>;
     p.part_ml = static_cast<float2 *>(ws);
     p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + prefix_ml_bytes(p));
     if (p.ctas_used > 0) {
         // absent tensors: a map that no copy uses
-        const bool own = p.Nc > 0, raw = p.W > 0 && p.Lkv > 0;
         CUtensorMap mqp, mqo, mkp, mvp, mkc, mvc, mkr, mvr;
         bool ok = make_map(&mqp, q, D, p.Hq, p.B * p.Lq, 1, p.hpt, p.tpt);
-        ok &= make_map(&mqo, q, D, p.Hq, p.Lq, p.B, p.hpt, p.tpt);
-        ok &= make_map(&mkp, p.Np ? kp : q, D, p.Hkv, p.Np ? p.Np : 1, 1, 1, kPfBN);
-        ok &= make_map(&mvp, p.Np ? vp : q, D, p.Hkv, p.Np ? p.Np : 1, 1, 1, kPfBN);
-        ok &= make_map(&mkc, own ? kc : q, D, p.Hkv, own ? p.Nc : 1, own ? p.B : 1, 1, kPfBN);
-        ok &= make_map(&mvc, own ? vc : q, D, p.Hkv, own ? p.Nc : 1, own ? p.B : 1, 1, kPfBN);
-        ok &= make_map(&mkr, raw ? kr : q, D, p.Hkv, raw ? p.Lkv : 1, raw ? p.B : 1, 1, kPfBN);
-        ok &= make_map(&mvr, raw ? vr : q, D, p.Hkv, raw ? p.Lkv : 1, raw ? p.B : 1, 1, kPfBN);
+        if (p.p_pieces > 0) {
+            ok &= make_map(&mkp, kp, D, p.Hkv, p.Np, 1, 1, kPfBN);
+            ok &= make_map(&mvp, vp, D, p.Hkv, p.Np, 1, 1, kPfBN);
+        } else {
+            mkp = mvp = mqp;
+        }
+        if (p.o_total > 0)
+            ok &= make_map(&mqo, q, D, p.Hq, p.Lq, p.B, p.hpt, p.tpt);
+        else
+            mqo = mqp;
+        if (p.Nc > 0) {
+            ok &= make_map(&mkc, kc, D, p.Hkv, p.Nc, p.B, 1, kPfBN);
+            ok &= make_map(&mvc, vc, D, p.Hkv, p.Nc, p.B, 1, kPfBN);
+        } else {
+            mkc = mvc = mqp;
+        }
+        if (p.W > 0) {
+            ok &= make_map(&mkr, kr, D, p.Hkv, p.Lkv, p.B, 1, kPfBN);
+            ok &= make_map(&mvr, vr, D, p.Hkv, p.Lkv, p.B, 1, kPfBN);
+        } else {
+            mkr = mvr = mqp;
+        }
         if (!ok)
             return cudaErrorInvalidValue;
-        const size_t smem = 1024 + SM::BYTES;
-        auto kern = prefix_attn_kernel<D>;
         // one CTA per SM: it takes all of the tensor memory
-        const size_t ask = smem < 120 * 1024 ? 120 * 1024 : smem;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
+        const size_t smem = 1024 + SM::BYTES < 120 * 1024 ? 120 * 1024 : 1024 + SM::BYTES;
+        auto kern = prefix_attn_kernel<D>;
+        int dev = -1;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess)
             return e;
-        e = check_reg_split(kern, kPfThreads, kPfSoftmaxThreads, kPfSoftmaxRegs, kPfOtherRegs);
-        if (e != cudaSuccess)
-            return e;
-        e = launch_pdl(kern, dim3((unsigned)p.ctas_used), dim3(kPfThreads), ask, stream, mqp, mqo, mkp, mvp, mkc, mvc,
-                       mkr, mvr, p);
+        if (!prefix_set_up(dev, D)) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess)
+                return e;
+            e = check_reg_split(kern, kPfThreads, kPfSoftmaxThreads, kPfSoftmaxRegs, kPfOtherRegs);
+            if (e != cudaSuccess)
+                return e;
+            if (dev < 64)
+                g_prefix_ready[D == 128].fetch_or(1ull << dev, std::memory_order_release);
+        }
+        e = launch_pdl(kern, dim3((unsigned)p.ctas_used), dim3(kPfThreads), smem, stream, mqp, mqo, mkp, mvp, mkc,
+                       mvc, mkr, mvr, p);
         if (e != cudaSuccess)
             return e;
     }
@@ -1066,30 +1087,12 @@ static cudaError_t launch_prefix_t(PrefixParams &p, const void *q, const void *k
                       stream, p);
 }
 
-cudaError_t launch_prefix_attn(int B, int Lq, int Lkv, int Hq, int Hkv, int d, int Np, int Nc, int m, int W,
-                               float scale, const int32_t *q_pos, const int32_t *kv_pos0, const void *q,
-                               const void *kp, const void *vp, const void *kc, const void *vc, const void *kr,
-                               const void *vr, void *o, float *lse, void *ws, cudaStream_t stream, int num_sms)
+static cudaError_t launch_prefix_attn(PrefixParams &p, int d, const void *q, const void *kp, const void *vp,
+                                      const void *kc, const void *vc, const void *kr, const void *vr, void *ws,
+                                      cudaStream_t stream)
 {
-    PrefixParams p = {};
-    p.B = B;
-    p.Lq = Lq;
-    p.Lkv = Lkv;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.Np = Np;
-    p.Nc = Nc;
-    p.m = m;
-    p.W = W;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.q_pos = q_pos;
-    p.kv_pos0 = kv_pos0;
-    p.o = static_cast<__nv_bfloat16 *>(o);
-    p.lse = lse;
-    if (!prefix_plan(p, d))
-        return cudaErrorInvalidValue;
-    return d == 128 ? launch_prefix_t<128>(p, q, kp, vp, kc, vc, kr, vr, ws, stream, num_sms)
-                    : launch_prefix_t<64>(p, q, kp, vp, kc, vc, kr, vr, ws, stream, num_sms);
+    return d == 128 ? launch_prefix_t<128>(p, q, kp, vp, kc, vc, kr, vr, ws, stream)
+                    : launch_prefix_t<64>(p, q, kp, vp, kc, vc, kr, vr, ws, stream);
 }
 
 }  // namespace hyb

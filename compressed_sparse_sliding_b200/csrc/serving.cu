@@ -12,9 +12,9 @@ static bool ws_ok(const void *ws, size_t ws_bytes, size_t need)
     return need == 0 || (ws && ws_bytes >= need && !(reinterpret_cast<uintptr_t>(ws) & 255u));
 }
 
-// Sizes shared by the workspace query and the call; HYB_OK when the call's
-// index arithmetic holds for them.
-static hyb_status check_prefix(const hyb_problem *p, int Np)
+// Sizes, tiling and split shared by the workspace query and the call; HYB_OK
+// when the call's index arithmetic holds for them.
+static hyb_status check_prefix(const hyb_problem *p, int Np, PrefixParams &a)
 {
     hyb_status st = check_problem(p, false);
     if (st != HYB_OK)
@@ -25,7 +25,20 @@ static hyb_status check_prefix(const hyb_problem *p, int Np)
     if (p->topk > 0 || (long long)p->B * p->Lq * p->Hq >= (1LL << 31) || (long long)Np + p->Nc >= (1LL << 30) ||
         p->W >= (1 << 30))
         return HYB_ERR_UNSUPPORTED;
-    return HYB_OK;
+    a = PrefixParams{};
+    a.B = p->B;
+    a.Lq = p->Lq;
+    a.Lkv = p->Lkv;
+    a.Hq = p->Hq;
+    a.Hkv = p->Hkv;
+    a.Np = Np;
+    a.Nc = p->Nc;
+    a.m = p->m;
+    a.W = p->W;
+    a.q_pos = p->q_pos;
+    a.kv_pos0 = p->kv_pos0;
+    a.scale_log2 = softmax_scale(p) * 1.4426950408889634f;
+    return prefix_plan(a, p->d) ? HYB_OK : HYB_ERR_UNSUPPORTED;
 }
 
 // Checks and launch shared by the two compaction entry points: t holds, per
@@ -76,9 +89,8 @@ extern "C" {
 
 size_t hyb_prefix_workspace_size(const hyb_problem *p, int Np)
 {
-    if (check_prefix(p, Np) != HYB_OK)
-        return 0;
-    return prefix_workspace_bytes(p->B, p->Lq, p->Lkv, p->Hq, p->Hkv, p->d, Np, p->Nc, p->W);
+    PrefixParams a;
+    return check_prefix(p, Np, a) == HYB_OK ? prefix_workspace(a, p->d) : 0;
 }
 
 hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, const void *kp, const void *vp,
@@ -86,7 +98,8 @@ hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, cons
                                float *lse, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
     NvtxRange nvtx_range("hyb_prefix_attn_fwd");
-    const hyb_status st = check_prefix(p, Np);
+    PrefixParams a;
+    const hyb_status st = check_prefix(p, Np, a);
     if (st != HYB_OK)
         return st;
     if (!q || !o || !aligned16(q) || !aligned16(o))
@@ -97,14 +110,11 @@ hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, cons
         return HYB_ERR_INVALID_ARG;
     if (p->W > 0 && (!k_raw || !v_raw || !aligned16(k_raw) || !aligned16(v_raw)))
         return HYB_ERR_INVALID_ARG;
-    const size_t need = hyb_prefix_workspace_size(p, Np);
-    if (need == ~(size_t)0)
-        return HYB_ERR_UNSUPPORTED;   // more key tiles than the split counts
-    if (!ws_ok(ws, ws_bytes, need))
+    if (!ws_ok(ws, ws_bytes, prefix_workspace(a, p->d)))
         return HYB_ERR_WORKSPACE;
-    return cuda_status(launch_prefix_attn(p->B, p->Lq, p->Lkv, p->Hq, p->Hkv, p->d, Np, p->Nc, p->m, p->W,
-                                          softmax_scale(p), p->q_pos, p->kv_pos0, q, kp, vp, kc, vc, k_raw,
-                                          v_raw, o, lse, ws, stream, num_sms_current()));
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.lse = lse;
+    return cuda_status(launch_prefix_attn(a, p->d, q, kp, vp, kc, vc, k_raw, v_raw, ws, stream));
 }
 
 hyb_status hyb_attn_weights(const hyb_problem *p, const void *q, const void *kc, const float *lse,
