@@ -25,7 +25,7 @@ def _select(hb, acc, n_keep, n_first=0, n_last=0, n_valid=None):
 @pytest.mark.parametrize("B,Nc,n_keep,n_first,n_last", [
     (1, 1, 1, 0, 0), (2, 2, 1, 0, 1), (3, 1000, 333, 1, 7), (2, 4099, 4098, 0, 0), (1, 9001, 100, 50, 50),
     (1, 70001, 20000, 4, 64), (150, 300, 128, 2, 2), (2, 33000, 16384, 0, 100), (1, 300001, 150000, 10, 10),
-    (5, 64, 100, 3, 3), (1, 5000, 1, 0, 0),
+    (5, 64, 100, 3, 3), (1, 5000, 1, 0, 0), (2, 20000, 19990, 9, 0), (40, 9000, 1000, 0, 30), (1, 600001, 250000, 3, 9),
 ])
 @pytest.mark.parametrize("kind", ["heavy", "ties"])
 def test_selection_matches_definition(hb, B, Nc, n_keep, n_first, n_last, kind):
