@@ -46,21 +46,56 @@
 
 namespace hyb {
 
+// The phase of the given parity has completed (a try may sleep for a while first).
+__device__ __forceinline__ bool mbar_test_wait(uint32_t addr, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait that tries the barrier some times before it looks at the clock
 // and the limit (a load from global memory, several hundred clocks): the waits
 // of these kernels are short and many.  Gives up when the CTA's abort flag is
-// up, like mbar_wait, which takes over afterwards.
-__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+// up, like mbar_wait, which takes over afterwards; `tries` is wait_tries().
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int tries)
 {
     const uint32_t addr = smem_u32(bar);
 #pragma unroll 1
-    for (int it = 0; it < 64; ++it) {
+    for (int it = 0; it < tries; ++it) {
         if (mbar_try_wait(addr, parity))
             return true;
         if (*abort_flag)
             return false;
     }
+    if (tries == 0 && !mbar_test_wait(addr, parity)) {
+        // a shortened limit: felt at once, also by waits that a try would sleep through
+        const uint64_t t0 = global_ns();
+        const uint64_t lim = *reinterpret_cast<volatile uint64_t *>(&g_wait_limit_ns);
+        while (!mbar_test_wait(addr, parity)) {
+            if (*abort_flag)
+                return false;
+            if (global_ns() - t0 > lim) {
+                set_error(HYB_ERR_DEVICE_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+        return true;
+    }
     return mbar_wait(bar, parity, abort_flag);
+}
+
+// None where the limit has been shortened.
+__device__ __forceinline__ int wait_tries()
+{
+    return *reinterpret_cast<volatile uint64_t *>(&g_wait_limit_ns) >= kWaitLimitNs ? 64 : 0;
 }
 
 // One lane of the (converged) warp.
@@ -162,14 +197,14 @@ struct PrefixSmem {
     static constexpr int OFF_TOK = OFF_MAX + kPfSoftmaxThreads * 4;
     static constexpr int OFF_ITEM = OFF_TOK + kPfItemSlots * 256 * (int)sizeof(PrefixToken);
     static constexpr int OFF_BAR = (OFF_ITEM + kPfItemSlots * (int)sizeof(PrefixItem) + 15) / 16 * 16;
-    static constexpr int OFF_MISC = OFF_BAR + 32 * 8;
+    static constexpr int OFF_MISC = OFF_BAR + 40 * 8;
     static constexpr int BYTES = OFF_MISC + 16 * 4;
 };
 static_assert(1024 + PrefixSmem<128>::BYTES <= 227 * 1024, "shared memory of a CTA");
 
 // barrier slots (two each from PB_KF on, three item slots)
 enum { PB_QF = 0, PB_QE = 1, PB_KF = 2, PB_KE = 4, PB_VF = 6, PB_VE = 8, PB_SF = 10, PB_PF = 12, PB_OF = 14,
-       PB_OE = 16, PB_IF = 18, PB_IE = 21, PB_DONE = 24 };
+       PB_OE = 16, PB_IF = 18, PB_IE = 21, PB_DONE = 24, PB_MEET = 25 };
 
 // Entries visible to position pos: those ending before its window.
 __device__ __forceinline__ int pf_visible(long long pos, int m, int W, int n)
@@ -320,6 +355,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             mbar_init(&bar[PB_IE + s], 19);    // producer, MMA and softmax warps
         }
         mbar_init(&bar[PB_DONE], 2);
+        for (int s = 0; s < 8; ++s)
+            mbar_init(&bar[PB_MEET + s], 2);
         mbar_fence_init();
         misc[1] = 0;
     }
@@ -331,9 +368,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
     const uint32_t tmem = (uint32_t)misc[0];
     pdl_wait();      // launched as a programmatic dependent: the previous kernel's writes
     pdl_trigger();   // are visible from here on; the next kernel may start its launch
+    const int tries = wait_tries();
     // every lane waits; the warp goes on only if all of them got through
     auto wait = [&](int b, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_short(&bar[b], parity, abort_flag)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_short(&bar[b], parity, abort_flag, tries)) != 0;
     };
     // the n-th item of this CTA (false: none, or giving up); `release` after its last read
     auto item = [&](uint32_t n, PrefixItem &it) {
@@ -394,7 +432,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         while (ok && item(nq, it)) {
             release(nq);
             if (lane == 0) {
-                ok = nq == 0 || mbar_wait_short(&bar[PB_QE], (nq - 1) & 1, abort_flag);
+                ok = nq == 0 || mbar_wait_short(&bar[PB_QE], (nq - 1) & 1, abort_flag, tries);
                 if (ok) {
                     mbar_arrive_expect_tx(&bar[PB_QF], (1 + it.val1) * q_bytes);
 #pragma unroll
@@ -418,7 +456,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                                                         : (!ent ? &tm_kr : it.pre ? &tm_kp : &tm_kc);
                             const uint32_t st = cnt % kPfStages;
                             if (cnt >= kPfStages &&
-                                !mbar_wait_short(&empty[st], ((cnt / kPfStages) - 1) & 1, abort_flag)) {
+                                !mbar_wait_short(&empty[st], ((cnt / kPfStages) - 1) & 1, abort_flag, tries)) {
                                 ok = false;
                                 break;
                             }
@@ -428,7 +466,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                             // has, since Q was reloaded), so that a warp that has seen K of
                             // tile n is at most one phase of V behind.
                             if (!kv && j < 2 && cnt >= kPfStages &&
-                                !mbar_wait_short(&bar[PB_VF + st], ((cnt / kPfStages) - 1) & 1, abort_flag)) {
+                                !mbar_wait_short(&bar[PB_VF + st], ((cnt / kPfStages) - 1) & 1, abort_flag, tries)) {
                                 ok = false;
                                 break;
                             }
@@ -561,8 +599,15 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         const uint32_t tO = tl + TM_O + x * 128 + half * (D / 2);
         float *mine = reinterpret_cast<float *>(smem + SM::OFF_MAX) + threadIdx.x;
         const float *other = reinterpret_cast<float *>(smem + SM::OFF_MAX) + (threadIdx.x ^ 128);
-        // the two warps of a row quad meet (barriers 1 .. 8)
-        auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + x * 4 + quad) : "memory"); };
+        // the two warps of a row quad meet: bounded, like every wait (a named barrier
+        // would keep one of them for ever if the other gave up)
+        uint32_t met = 0;
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bar[PB_MEET + x * 4 + quad]);
+            return wait(PB_MEET + x * 4 + quad, met++ & 1);
+        };
         uint8_t *stage = smem + SM::OFF_ST + warp * SM::STAGE_BYTES;
         const int rtok = row / p.hpt, rhead = row % p.hpt;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
@@ -631,7 +676,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                         tmax = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]));
                     }
                     *mine = tmax;
-                    meet();
+                    if (!(ok = meet()))
+                        break;
                     tmax = fmaxf(tmax, *other);
                     tmax *= p.scale_log2;  // the scale is positive
                     // the reference maximum moves (and O is rescaled) only when a
@@ -712,9 +758,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             }
             if (warp_rows) {
                 *mine = l_sum;
-                meet();
+                if (!(ok = meet()))
+                    break;
                 l_sum += *other;
-                meet();          // before the next item's first maximum
+                if (!(ok = meet()))      // before the next item's first maximum
+                    break;
             }
             const long long at = (long long)(it.part + (it.pair ? 0 : x)) * p.rows + (long long)flat * p.Hq + h;
             if (valid_row && half == 0)

@@ -11,16 +11,17 @@
 // HBM bounds it, with many (the last tokens of a prompt) the exponentials.
 //
 // Layout.  S^T = K Q^T on tcgen05: keys are the MMA's M, so a TMEM lane is a key
-// and the sum over query rows stays inside one thread (no reduction across
-// threads, no atomics between CTAs: each entry has one owner, and equal calls
-// give equal bits).  A CTA owns a run of key-tile pairs of one or more sequences;
-// two epilogue warpgroups take one tile of the pair each, from two S buffers a
-// tile (4 x 128 TMEM columns), so the MMA of the next query block runs under
-// the exponentials of this one.  Query blocks (hpt heads x tpt tokens, up to
-// 128 rows) stay in shared memory for the whole run where all of a sequence's
-// fit 64 KB (decode), and stream through the same slots otherwise.
+// and the sum over query rows stays inside one thread but for the two epilogue
+// warpgroups, which take alternate 32-row column chunks of S^T and add their two
+// sums through shared memory.  No atomics between CTAs: each entry has one owner,
+// and equal calls give equal bits.  A CTA owns a run of key tiles of one or more
+// sequences, every CTA the same number of tiles that hold visible entries.  Four
+// K stages and four S buffers (4 x 128 TMEM columns) keep copies, MMAs and
+// exponentials of different tiles running together.  Query blocks (hpt heads x
+// tpt tokens, up to 128 rows) stay in shared memory for the whole run where all
+// of a sequence's fit 64 KB (decode), and stream through the same slots otherwise.
 //
-// Roles (512 threads): warps 0-3 / 4-7 epilogue of tile A / B (thread = key),
+// Roles (512 threads): warps 0-3 / 4-7 epilogue (thread = key, even / odd chunks),
 // warp 8 TMA producer, warp 9 MMA issue, warp 10 writes each query block's lse
 // and visible counts beside it, warps 12-15 gather the selected rows with
 // cp.async when idx is given (16 lanes per row).
@@ -31,16 +32,22 @@ namespace hyb {
 constexpr int kAwThreads = 512;
 constexpr int kAwBM = 128;          // keys of a tile
 constexpr int kAwKStages = 4;
+constexpr int kAwSBufs = 4;
 constexpr int kAwQBytes = 64 * 1024;
 constexpr int kAwQStages = 16;      // barrier slots; the bytes usually bind first
+// Sequences whose visible counts a CTA sums up at its start, to cut the stream of
+// all visible tiles evenly, and the positions it reads for that; with more, a
+// CTA's share counts full caches and its many sequences even out.
+constexpr int kAwCounted = 1024, kAwPositions = 8192;
+constexpr int kAwZero = 4096;       // entries zeroed at a time
 
 struct WeightParams {
     int B, Lq, Hq, Hkv, g, Nc, m, W, e0, K;
     int hpt, tpt, nht, nblk;        // heads and tokens of a query block, head tiles, blocks per KV head
     int NB;                         // MMA columns of a block (rows rounded up to 16)
     int nqs, resident;              // query slots; all blocks of a sequence fit them
-    int pairs;                      // key-tile pairs of a full cache (idx: of the selection)
-    long long total;                // B * pairs
+    int tiles;                      // key tiles of a full cache (idx: of the selection)
+    int counted;                    // runs by visible tiles (see kAwCounted)
     int accumulate;
     float scale_log2;
     const int32_t *q_pos, *idx;
@@ -56,21 +63,24 @@ struct WeightSmem {
     static constexpr int OFF_K = kAwQBytes;
     static constexpr int OFF_COL = OFF_K + kAwKStages * K_BYTES;     // -lse (log2) per column, then counts
     static constexpr int NCOL = kAwQBytes / (D * 2);                 // columns of all slots together
-    static constexpr int OFF_BAR = OFF_COL + NCOL * 8;
+    static constexpr int OFF_SUM = OFF_COL + NCOL * 8;               // [2][128] sums of the second warpgroup
+    static constexpr int OFF_NV = OFF_SUM + 2 * kAwBM * 4;           // [kAwCounted] visible entries
+    static constexpr int OFF_CUM = OFF_NV + kAwCounted * 4;          // [kAwCounted + 1] visible tiles before
+    static constexpr int OFF_BAR = OFF_CUM + (kAwCounted + 4) * 4;
     static constexpr int OFF_MISC = OFF_BAR + 64 * 8;
     static constexpr int BYTES = OFF_MISC + 128;
 };
+static_assert(1024 + WeightSmem<128>::BYTES <= 227 * 1024, "shared memory of a CTA");
 
 // barrier slots
-enum { WB_QF = 0, WB_QE = 16, WB_KF = 32, WB_KE = 36, WB_SF = 40, WB_SE = 44, WB_DONE = 48 };
+enum { WB_QF = 0, WB_QE = 16, WB_KF = 32, WB_KE = 36, WB_SF = 40, WB_SE = 44, WB_TF = 48, WB_TE = 50, WB_DONE = 52 };
 
-// A stretch of one sequence's key-tile pairs, the work of a CTA between two
-// sequence changes.
+// A stretch of one sequence's key tiles, the work of a CTA between two sequence
+// changes.
 struct WeightRun {
     int b, nv;         // sequence; entries that some query token of it sees
-    int ntiles;        // key tiles (idx: of the selection)
-    int lo, hi;        // pairs of this run
-    int z0, z1;        // entries this run zeroes (those no query token sees)
+    int lo, hi;        // key tiles of this run
+    int z0, z1;        // entries this run zeroes (not counted: those no query token sees)
 };
 
 __device__ __forceinline__ int aw_visible(const WeightParams &p, int flat)
@@ -80,40 +90,77 @@ __device__ __forceinline__ int aw_visible(const WeightParams &p, int flat)
     return max(nv - p.e0, 0);
 }
 
-// The run that starts at pair u of the CTA's range [u, end) of the stream of all
-// sequences' pairs, which counts full caches: a sequence's pairs that hold
-// visible entries are spread over its share of the range.  Whole warp.
-__device__ __forceinline__ WeightRun weight_run(const WeightParams &p, long long u, long long end, int lane,
-                                                long long &next)
+__device__ __forceinline__ int aw_tiles(const WeightParams &p, int nv)
 {
-    WeightRun r;
-    r.b = (int)(u / p.pairs);
-    const int a0 = (int)(u % p.pairs);
-    const int a1 = (int)min((long long)p.pairs, a0 + (end - u));
-    next = u + (a1 - a0);
-    int nv = 0;
-    for (int t = lane; t < p.Lq; t += 32)
-        nv = max(nv, aw_visible(p, r.b * p.Lq + t));
-    r.nv = __reduce_max_sync(0xffffffffu, nv);
-    r.ntiles = ((p.idx ? p.K : r.nv) + kAwBM - 1) / kAwBM;
-    const long long T = (r.ntiles + 1) / 2;
-    r.lo = (int)(T * a0 / p.pairs);
-    r.hi = (int)(T * a1 / p.pairs);
-    r.z0 = r.z1 = 0;
-    if (!p.accumulate && !p.idx) {
-        r.z0 = r.nv + (int)((long long)(p.Nc - r.nv) * a0 / p.pairs);
-        r.z1 = r.nv + (int)((long long)(p.Nc - r.nv) * a1 / p.pairs);
-    }
-    return r;
+    return ((p.idx ? p.K : nv) + kAwBM - 1) / kAwBM;
 }
+
+// Walks a CTA's runs (whole warp; every role walks the same ones).
+struct WeightWalk {
+    long long u, end;
+    int b;
+    const int *nvs, *cum;
+
+    __device__ __forceinline__ WeightWalk(const WeightParams &p, const int *nv_, const int *cum_)
+        : b(0), nvs(nv_), cum(cum_)
+    {
+        const long long total = p.counted ? cum[p.B] : (long long)p.B * p.tiles;
+        u = total * blockIdx.x / gridDim.x;
+        end = total * (blockIdx.x + 1) / gridDim.x;
+        if (p.counted && u < end) {
+            // the sequence of tile u: the last one with cum <= u
+            int lo = 0, hi = p.B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cum[mid] <= (int)u)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            b = lo;
+        }
+    }
+
+    __device__ __forceinline__ bool next(const WeightParams &p, int lane, WeightRun &r)
+    {
+        if (u >= end)
+            return false;
+        r.z0 = r.z1 = 0;
+        if (p.counted) {
+            while (cum[b + 1] <= (int)u)
+                ++b;
+            r.b = b;
+            r.nv = nvs[b];
+            r.lo = (int)u - cum[b];
+            r.hi = min(cum[b + 1], (int)end) - cum[b];
+            u += r.hi - r.lo;
+            return true;
+        }
+        // shares of full caches: a sequence's visible tiles are spread over its share
+        r.b = (int)(u / p.tiles);
+        const int a0 = (int)(u % p.tiles);
+        const int a1 = (int)min((long long)p.tiles, a0 + (end - u));
+        u += a1 - a0;
+        int nv = 0;
+        for (int t = lane; t < p.Lq; t += 32)
+            nv = max(nv, aw_visible(p, r.b * p.Lq + t));
+        r.nv = __reduce_max_sync(0xffffffffu, nv);
+        const long long T = aw_tiles(p, r.nv);
+        r.lo = (int)(T * a0 / p.tiles);
+        r.hi = (int)(T * a1 / p.tiles);
+        if (!p.accumulate && !p.idx) {
+            r.z0 = r.nv + (int)((long long)(p.Nc - r.nv) * a0 / p.tiles);
+            r.z1 = r.nv + (int)((long long)(p.Nc - r.nv) * a1 / p.tiles);
+        }
+        return true;
+    }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kAwThreads, 1)
 attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const WeightParams p)
 {
-    pdl_wait();      // launched as a programmatic dependent: the previous kernel's writes
-    pdl_trigger();   // are visible from here on; the next kernel may start its launch
     using SM = WeightSmem<D>;
     constexpr int NCB = D / 64;
     extern __shared__ __align__(1024) uint8_t aw_smem_raw[];
@@ -123,6 +170,9 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint8_t *sK = smem + SM::OFF_K;
     float *sLse = reinterpret_cast<float *>(smem + SM::OFF_COL);       // -lse, log2 units, per slot and column
     int *sNv = reinterpret_cast<int *>(smem + SM::OFF_COL + SM::NCOL * 4);
+    float *sSum = reinterpret_cast<float *>(smem + SM::OFF_SUM);
+    int *sSeq = reinterpret_cast<int *>(smem + SM::OFF_NV);
+    int *sCum = reinterpret_cast<int *>(smem + SM::OFF_CUM);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + SM::OFF_BAR);
     int *misc = reinterpret_cast<int *>(smem + SM::OFF_MISC);
     int *sMin = misc + 8;                                              // [16] least count of a slot's columns
@@ -138,64 +188,100 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int s = 0; s < kAwKStages; ++s) {
             mbar_init(&bar[WB_KF + s], p.idx ? 128 : 1);
             mbar_init(&bar[WB_KE + s], 1);
+        }
+        for (int s = 0; s < kAwSBufs; ++s) {
             mbar_init(&bar[WB_SF + s], 1);
-            mbar_init(&bar[WB_SE + s], 128);
+            mbar_init(&bar[WB_SE + s], 8);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar[WB_TF + s], 4);         // the second warpgroup's sums
+            mbar_init(&bar[WB_TE + s], 4);
         }
         mbar_init(&bar[WB_DONE], 1);
         mbar_fence_init();
         misc[1] = 0;
     }
+    for (int b = threadIdx.x; p.counted && b < p.B; b += kAwThreads)
+        sSeq[b] = 0;
     if (warp == 9)
         tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[0];
+    pdl_wait();      // launched as a programmatic dependent: the previous kernel's writes
+    pdl_trigger();   // are visible from here on; the next kernel may start its launch
+    const int tries = wait_tries();
+    if (p.counted) {
+        const int n = p.B * p.Lq;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += kAwThreads) {
+            const int nv = aw_visible(p, i);
+            if (nv > 0)
+                atomicMax(&sSeq[p.Lq == 1 ? i : i / p.Lq], nv);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int before = 0;
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int b = b0 + lane;
+                int t = b < p.B ? aw_tiles(p, sSeq[b]) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, t, o);
+                    t += lane >= o ? x : 0;
+                }
+                if (b < p.B)
+                    sCum[b + 1] = before + t;
+                before += __shfl_sync(0xffffffffu, t, 31);
+            }
+            if (lane == 0)
+                sCum[0] = 0;
+        }
+        __syncthreads();
+    }
 
-    const long long u0 = p.total * blockIdx.x / gridDim.x, u1 = p.total * (blockIdx.x + 1) / gridDim.x;
     const uint32_t qbytes = (uint32_t)p.NB * D * 2;
     const int nblocks = p.Hkv * p.nblk;            // query blocks of a sequence
     // Query slot and fill count of the n-th block use: with resident blocks a
     // slot is filled once a run, otherwise the blocks go round the slots.
     auto wait = [&](int b, uint32_t parity) {      // whole warp
-        return __all_sync(0xffffffffu, mbar_wait(&bar[b], parity, abort_flag)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_short(&bar[b], parity, abort_flag, tries)) != 0;
     };
+    WeightWalk walk(p, sSeq, sCum);
+    WeightRun r;
+    bool ok = true;
 
     if (warp == 8 || warp == 10) {
         // ============ query blocks: copies (warp 8), lse and counts (warp 10); K tiles (warp 8) ============
         uint32_t kc = 0, qc = 0, runs = 0;
-        bool ok = true;
         const uint32_t box_bytes = (uint32_t)p.hpt * p.tpt * D * 2;
-        for (long long u = u0; ok && u < u1;) {
-            const WeightRun r = weight_run(p, u, u1, lane, u);
-            for (int pr = r.lo; ok && pr < r.hi; ++pr) {
+        while (ok && walk.next(p, lane, r)) {
+            for (int tile = r.lo; ok && tile < r.hi; ++tile) {
                 for (int i = 0; ok && i < nblocks; ++i) {
-                    const int h = i / p.nblk, blk = i % p.nblk;
-                    if (warp == 8 && blk == 0 && !p.idx) {
-                        for (int tile = 2 * pr; ok && tile < min(2 * pr + 2, r.ntiles); ++tile) {
-                            const uint32_t st = kc % kAwKStages;
-                            if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
-                                break;
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(&bar[WB_KF + st], SM::K_BYTES);
-                                for (int cb = 0; cb < NCB; ++cb)
-                                    tma_load_4d(sK + st * SM::K_BYTES + cb * kAwBM * 128, &tm_k, &bar[WB_KF + st],
-                                                cb * 64, h, tile * kAwBM, r.b);
-                            }
-                            __syncwarp();
-                            ++kc;
-                        }
-                        if (!ok)
+                    const int h = i / p.nblk, blk = i - h * p.nblk;
+                    const bool load_k = warp == 8 && blk == 0 && !p.idx;
+                    const bool load_q = !p.resident || tile == r.lo;
+                    if (load_k) {
+                        const uint32_t st = kc % kAwKStages;
+                        if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
                             break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&bar[WB_KF + st], SM::K_BYTES);
+                            for (int cb = 0; cb < NCB; ++cb)
+                                tma_load_4d(sK + st * SM::K_BYTES + cb * kAwBM * 128, &tm_k, &bar[WB_KF + st],
+                                            cb * 64, h, tile * kAwBM, r.b);
+                        }
+                        __syncwarp();
+                        ++kc;
                     }
-                    if (p.resident && pr > r.lo)
+                    if (!load_q)
                         continue;
                     const uint32_t st = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
-                    if (fill > 0 && !(ok = wait(WB_QE + st, (fill - 1) & 1)))
-                        break;
-                    ++qc;
                     const int t0 = (blk / p.nht) * p.tpt, h0 = (blk % p.nht) * p.hpt;
                     if (warp == 8) {
+                        if (fill > 0 && !(ok = wait(WB_QE + st, (fill - 1) & 1)))
+                            break;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&bar[WB_QF + st], box_bytes);
                             for (int cb = 0; cb < NCB; ++cb)
@@ -204,25 +290,37 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         }
                         __syncwarp();
                     } else {
-                        int least = INT_MAX;
-                        for (int c = lane; c < p.NB; c += 32) {
+                        // up to four columns a lane, all loads before the slot's wait
+                        float l[4];
+                        int nv[4], least = INT_MAX;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int c = lane + 32 * k;
                             const int t = t0 + c / p.hpt, hd = h0 + c % p.hpt;
-                            float l = 0.f;
-                            int nv = 0;
+                            l[k] = 0.f;
+                            nv[k] = 0;
                             if (c < p.hpt * p.tpt && t < p.Lq && hd < p.g) {
-                                l = -1.4426950408889634f *
-                                    p.lse[((size_t)r.b * p.Hq + h * p.g + hd) * p.Lq + t];
-                                nv = aw_visible(p, r.b * p.Lq + t);
-                                least = min(least, nv);
+                                l[k] = p.lse[((size_t)r.b * p.Hq + h * p.g + hd) * p.Lq + t];
+                                nv[k] = p.Lq == 1 ? r.nv : aw_visible(p, r.b * p.Lq + t);
+                                least = min(least, nv[k]);
                             }
-                            sLse[st * p.NB + c] = l;
-                            sNv[st * p.NB + c] = nv;
                         }
                         least = __reduce_min_sync(0xffffffffu, least);
+                        if (fill > 0 && !(ok = wait(WB_QE + st, (fill - 1) & 1)))
+                            break;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int c = lane + 32 * k;
+                            if (c < p.NB) {
+                                sLse[st * p.NB + c] = -1.4426950408889634f * l[k];
+                                sNv[st * p.NB + c] = nv[k];
+                            }
+                        }
                         if (lane == 0)
                             sMin[st] = least;
                         mbar_arrive(&bar[WB_QF + st]);
                     }
+                    ++qc;
                 }
             }
             if (r.hi > r.lo)
@@ -245,38 +343,42 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         if (p.idx) {
             constexpr int CH = D / 8;              // 16-byte chunks of a row
             constexpr int RPI = 128 / CH;          // rows a pass
+            constexpr int N = kAwBM / RPI;
             const int pt = threadIdx.x - 12 * 32;
             const int c8 = pt % CH, rsub = pt / CH;
             const uint32_t dchunk = (c8 >> 3) * kAwBM * 128;
             uint32_t kc = 0;
-            bool ok = true;
-            for (long long u = u0; ok && u < u1;) {
-                const WeightRun r = weight_run(p, u, u1, lane, u);
-                for (int pr = r.lo; ok && pr < r.hi; ++pr)
-                    for (int h = 0; ok && h < p.Hkv; ++h)
-                        for (int tile = 2 * pr; tile < min(2 * pr + 2, r.ntiles); ++tile) {
-                            int src[kAwBM / RPI];
+            while (ok && walk.next(p, lane, r)) {
+                for (int tile = r.lo; ok && tile < r.hi; ++tile) {
+                    int src[N];
 #pragma unroll
-                            for (int i = 0; i < kAwBM / RPI; ++i) {
-                                const int slot = tile * kAwBM + i * RPI + rsub;
-                                const int e = slot < p.K ? p.idx[(size_t)r.b * p.K + slot] : -1;
-                                if (e >= p.Nc && c8 == 0 && h == 0)
-                                    set_error(HYB_ERR_DEVICE_BOUNDS);
-                                src[i] = e < r.nv ? e : -1;
-                            }
-                            const uint32_t st = kc % kAwKStages;
-                            if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
-                                break;
-                            const uint32_t dst = smem_u32(sK + st * SM::K_BYTES) + dchunk;
+                    for (int i = 0; i < N; ++i) {
+                        const int slot = tile * kAwBM + i * RPI + rsub;
+                        src[i] = slot < p.K ? __ldg(p.idx + (size_t)r.b * p.K + slot) : -1;
+                    }
+                    bool bad = false;
 #pragma unroll
-                            for (int i = 0; i < kAwBM / RPI; ++i)
-                                cp_async_16(dst + sw128_offset(i * RPI + rsub, c8 & 7),
-                                            p.kc + (((size_t)r.b * p.Nc + max(src[i], 0)) * p.Hkv + h) * D + c8 * 8,
-                                            src[i] >= 0 ? 16u : 0u);
-                            cp_async_mbar_arrive(&bar[WB_KF + st]);
-                            mbar_arrive(&bar[WB_KF + st]);
-                            ++kc;
-                        }
+                    for (int i = 0; i < N; ++i) {
+                        bad |= src[i] >= p.Nc;
+                        src[i] = src[i] < r.nv ? src[i] : -1;
+                    }
+                    if (bad && c8 == 0)
+                        set_error(HYB_ERR_DEVICE_BOUNDS);
+                    for (int h = 0; h < p.Hkv; ++h) {
+                        const uint32_t st = kc % kAwKStages;
+                        if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
+                            break;
+                        const uint32_t dst = smem_u32(sK + st * SM::K_BYTES) + dchunk;
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            cp_async_16(dst + sw128_offset(i * RPI + rsub, c8 & 7),
+                                        p.kc + (((size_t)r.b * p.Nc + max(src[i], 0)) * p.Hkv + h) * D + c8 * 8,
+                                        src[i] >= 0 ? 16u : 0u);
+                        cp_async_mbar_arrive(&bar[WB_KF + st]);
+                        mbar_arrive(&bar[WB_KF + st]);
+                        ++kc;
+                    }
+                }
             }
             cp_async_wait_group<0>();
         }
@@ -284,150 +386,163 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // ================================ MMA issue ================================
         const uint32_t idesc = idesc_bf16(kAwBM, p.NB, false, false);
         const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK);
-        uint32_t kc = 0, qc = 0, runs = 0, sc[2] = {0, 0};
-        bool ok = true;
-        for (long long u = u0; ok && u < u1;) {
-            const WeightRun r = weight_run(p, u, u1, lane, u);
-            for (int pr = r.lo; ok && pr < r.hi; ++pr) {
-                const int nt = min(2, r.ntiles - 2 * pr);
+        uint32_t kc = 0, qc = 0, runs = 0, sc = 0;
+        const bool leader = elect_one();
+        while (ok && walk.next(p, lane, r)) {
+            for (int tile = r.lo; ok && tile < r.hi; ++tile) {
                 for (int i = 0; ok && i < nblocks; ++i) {
                     const int blk = i % p.nblk;
                     const uint32_t qs = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
+                    const uint32_t ks = kc % kAwKStages, buf = sc % kAwSBufs;
                     if (!(ok = wait(WB_QF + qs, fill & 1)))
                         break;
                     ++qc;
-                    for (int x = 0; ok && x < nt; ++x) {
-                        const uint32_t ks = (kc + x) % kAwKStages, buf = sc[x] & 1;
-                        if (blk == 0) {
-                            if (!(ok = wait(WB_KF + ks, ((kc + x) / kAwKStages) & 1)))
-                                break;
-                            if (p.idx)
-                                fence_proxy_async_smem();   // rows written by cp.async, read by the MMA
-                        }
-                        if (sc[x] >= 2 && !(ok = wait(WB_SE + 2 * x + buf, ((sc[x] >> 1) - 1) & 1)))
+                    if (blk == 0) {
+                        if (!(ok = wait(WB_KF + ks, (kc / kAwKStages) & 1)))
                             break;
-                        tc_fence_after();
-                        if (lane == 0) {
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint64_t da = sw128_desc(aK + ks * SM::K_BYTES + (kk >> 2) * kAwBM * 128 +
-                                                                   (kk & 3) * 32,
-                                                               16, 1024);
-                                const uint64_t db = sw128_desc(aQ + qs * qbytes + (kk >> 2) * p.NB * 128 +
-                                                                   (kk & 3) * 32,
-                                                               16, 1024);
-                                mma_bf16_ss(tmem + x * 256 + buf * 128, da, db, idesc, kk > 0 ? 1u : 0u);
-                            }
-                            mma_commit(&bar[WB_SF + 2 * x + buf]);
-                            if (blk == p.nblk - 1)
-                                mma_commit(&bar[WB_KE + ks]);
-                        }
-                        ++sc[x];
+                        if (p.idx)
+                            fence_proxy_async_smem();   // rows written by cp.async, read by the MMA
                     }
-                    if (!ok)
+                    if (sc >= kAwSBufs && !(ok = wait(WB_SE + buf, ((sc / kAwSBufs) - 1) & 1)))
                         break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t da = sw128_desc(aK + ks * SM::K_BYTES + (kk >> 2) * kAwBM * 128 +
+                                                               (kk & 3) * 32,
+                                                           16, 1024);
+                            const uint64_t db = sw128_desc(aQ + qs * qbytes + (kk >> 2) * p.NB * 128 + (kk & 3) * 32,
+                                                           16, 1024);
+                            mma_bf16_ss(tmem + buf * 128, da, db, idesc, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit(&bar[WB_SF + buf]);
+                        if (blk == p.nblk - 1)
+                            mma_commit(&bar[WB_KE + ks]);
+                        if (!p.resident || tile == r.hi - 1)
+                            mma_commit(&bar[WB_QE + qs]);
+                    }
+                    __syncwarp();
+                    ++sc;
                     if (blk == p.nblk - 1)
-                        kc += nt;
-                    if (lane == 0 && (!p.resident || pr == r.hi - 1))
-                        mma_commit(&bar[WB_QE + qs]);
+                        ++kc;
                 }
             }
             if (r.hi > r.lo)
                 ++runs;
         }
-        if (lane == 0) {
+        if (leader)
             mma_commit(&bar[WB_DONE]);
-            drain_wait(&bar[WB_DONE], 0);
-        }
+        __syncwarp();
+        drain_wait(&bar[WB_DONE], 0);
     } else if (warp < 8) {
         // ============================ exponentials and sums ============================
         const int x = warp >> 2;
         const int quad = warp & 3;
         const int key = quad * 32 + lane;
-        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16) + x * 256;
+        const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        uint32_t qc = 0, runs = 0, sc = 0;
-        bool ok = true;
-        for (long long u = u0; ok && u < u1;) {
-            const WeightRun r = weight_run(p, u, u1, lane, u);
+        uint32_t qc = 0, runs = 0, sc = 0, tc = 0;
+        if (p.counted && !p.accumulate && !p.idx) {
+            // entries that no query token sees
+            const int per = (p.Nc + kAwZero - 1) / kAwZero;
+            for (int w = blockIdx.x; w < p.B * per; w += gridDim.x) {
+                const int b = w / per, c = (w - b * per) * kAwZero, end = min(p.Nc, c + kAwZero);
+                for (int j = max(sSeq[b], c) + (int)threadIdx.x; j < end; j += 256)
+                    p.acc[(size_t)b * p.Nc + j] = 0.f;
+            }
+        }
+        while (ok && walk.next(p, lane, r)) {
             for (int j = r.z0 + (int)threadIdx.x; j < r.z1; j += 256)
                 p.acc[(size_t)r.b * p.Nc + j] = 0.f;
-            for (int pr = r.lo; ok && pr < r.hi; ++pr) {
-                const int tile = 2 * pr + x;
-                const bool active = tile < r.ntiles;
+            for (int tile = r.lo; ok && tile < r.hi; ++tile) {
                 const int j = tile * kAwBM + key;        // entry, or slot of the selection
                 float tot = 0.f;
                 for (int i = 0; ok && i < nblocks; ++i) {
                     const int blk = i % p.nblk;
                     const uint32_t qs = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
+                    const uint32_t buf = sc % kAwSBufs;
                     ++qc;
-                    // an idle warpgroup waits too, so that it never releases a slot
-                    // ahead of the others
-                    if (!(ok = wait(WB_QF + qs, fill & 1)))
+                    if (!(ok = wait(WB_QF + qs, fill & 1) && wait(WB_SF + buf, (sc / kAwSBufs) & 1)))
                         break;
-                    if (active) {
-                        if (!(ok = wait(WB_SF + 2 * x + (sc & 1), (sc >> 1) & 1)))
-                            break;
-                        tc_fence_after();
-                        // rows of this block: whole tokens, or the heads of a group's last tile
-                        const int t0 = (blk / p.nht) * p.tpt, h0 = (blk % p.nht) * p.hpt;
-                        const int ncv = min(p.hpt, p.g - h0) * min(p.tpt, p.Lq - t0);
-                        const bool full = p.idx || (tile + 1) * kAwBM <= sMin[qs];
-                        const uint32_t tS = tl + (sc & 1) * 128;
-                        const float *nl = sLse + qs * p.NB;
-                        const int *cn = sNv + qs * p.NB;
+                    tc_fence_after();
+                    // rows of this block: whole tokens, or the heads of a group's last tile
+                    const int t0 = (blk / p.nht) * p.tpt, h0 = (blk % p.nht) * p.hpt;
+                    const int ncv = min(p.hpt, p.g - h0) * min(p.tpt, p.Lq - t0);
+                    const bool full = p.idx || (tile + 1) * kAwBM <= sMin[qs];
+                    const uint32_t tS = tl + buf * 128;
+                    const float *nl = sLse + qs * p.NB;
+                    const int *cn = sNv + qs * p.NB;
 #pragma unroll 1
-                        for (int c = 0; c < ncv; c += 32) {
-                            float sv[32];
-                            tmem_ld32(tS + c, sv);
-                            tmem_ld_wait();
-                            if (full && c + 32 <= ncv) {
-                                uint64_t s2[2] = {0ull, 0ull};
+                    for (int c = 32 * x; c < ncv; c += 64) {
+                        float sv[32];
+                        tmem_ld32(tS + c, sv);
+                        tmem_ld_wait();
+                        if (full && c + 32 <= ncv) {
+                            uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                                for (int q = 0; q < 32; q += 4) {
-                                    const ulonglong2 l2 = *reinterpret_cast<const ulonglong2 *>(nl + c + q);
-                                    float a0, a1, b0, b1;
-                                    f2_split(fma_f2(f2(sv[q], sv[q + 1]), sc2, l2.x), a0, a1);
-                                    f2_split(fma_f2(f2(sv[q + 2], sv[q + 3]), sc2, l2.y), b0, b1);
-                                    s2[0] = add_f2(s2[0], f2(ex2_approx(a0), ex2_approx(a1)));
-                                    s2[1] = add_f2(s2[1], f2(ex2_approx(b0), ex2_approx(b1)));
-                                }
-                                float a0, a1;
-                                f2_split(add_f2(s2[0], s2[1]), a0, a1);
-                                tot += a0 + a1;
-                            } else {
-                                // some columns are padding, or do not see every key of the tile
-                                float s = 0.f;
-#pragma unroll
-                                for (int q = 0; q < 32; ++q) {
-                                    const bool in = c + q < ncv && (p.idx || j < cn[c + q]);
-                                    const float e = ex2_approx(fmaf(sv[q], p.scale_log2, nl[min(c + q, p.NB - 1)]));
-                                    s += in ? e : 0.f;
-                                }
-                                tot += s;
+                            for (int q = 0; q < 32; q += 4) {
+                                const ulonglong2 l2 = *reinterpret_cast<const ulonglong2 *>(nl + c + q);
+                                float a0, a1, b0, b1;
+                                f2_split(fma_f2(f2(sv[q], sv[q + 1]), sc2, l2.x), a0, a1);
+                                f2_split(fma_f2(f2(sv[q + 2], sv[q + 3]), sc2, l2.y), b0, b1);
+                                s2[0] = add_f2(s2[0], f2(ex2_approx(a0), ex2_approx(a1)));
+                                s2[1] = add_f2(s2[1], f2(ex2_approx(b0), ex2_approx(b1)));
                             }
+                            float a0, a1;
+                            f2_split(add_f2(s2[0], s2[1]), a0, a1);
+                            tot += a0 + a1;
+                        } else {
+                            // some columns are padding, or do not see every key of the tile
+                            float s = 0.f;
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) {
+                                const int cc = min(c + q, p.NB - 1);
+                                const bool in = c + q < ncv && (p.idx || j < cn[cc]);
+                                const float e = ex2_approx(fmaf(sv[q], p.scale_log2, nl[cc]));
+                                s += in ? e : 0.f;
+                            }
+                            tot += s;
                         }
-                        tc_fence_before();
-                        mbar_arrive(&bar[WB_SE + 2 * x + (sc & 1)]);
-                        ++sc;
                     }
-                    if (!p.resident || pr == r.hi - 1) {
-                        __syncwarp();
-                        if (lane == 0)
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bar[WB_SE + buf]);
+                        if (!p.resident || tile == r.hi - 1)
                             mbar_arrive(&bar[WB_QE + qs]);   // this warp has read the slot's columns
                     }
+                    ++sc;
                 }
-                if (!ok || !active)
-                    continue;
-                if (p.idx) {
-                    const int e = j < p.K ? p.idx[(size_t)r.b * p.K + j] : -1;
-                    // an entry listed twice counts twice, whichever is added first
-                    if (e >= 0 && e < r.nv)
-                        atomicAdd(&p.acc[(size_t)r.b * p.Nc + e], tot);
-                } else if (j < r.nv) {
-                    float *a = &p.acc[(size_t)r.b * p.Nc + j];
-                    *a = p.accumulate ? *a + tot : tot;
+                if (!ok)
+                    break;
+                // the two warpgroups' sums meet
+                const uint32_t tb = tc & 1;
+                if (x == 1) {
+                    if (tc >= 2 && !(ok = wait(WB_TE + tb, ((tc >> 1) - 1) & 1)))
+                        break;
+                    sSum[tb * kAwBM + key] = tot;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bar[WB_TF + tb]);
+                } else {
+                    if (!(ok = wait(WB_TF + tb, (tc >> 1) & 1)))
+                        break;
+                    tot += sSum[tb * kAwBM + key];
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bar[WB_TE + tb]);
+                    if (p.idx) {
+                        const int e = j < p.K ? p.idx[(size_t)r.b * p.K + j] : -1;
+                        // an entry listed twice counts twice, whichever is added first
+                        if (e >= 0 && e < r.nv)
+                            atomicAdd(&p.acc[(size_t)r.b * p.Nc + e], tot);
+                    } else if (j < r.nv) {
+                        float *a = &p.acc[(size_t)r.b * p.Nc + j];
+                        *a = p.accumulate ? *a + tot : tot;
+                    }
                 }
+                ++tc;
             }
             if (r.hi > r.lo)
                 ++runs;
@@ -476,7 +591,8 @@ static cudaError_t launch_weights_t(WeightParams &p, const void *q, const void *
         if (e != cudaSuccess)
             return e;
     }
-    const long long grid = p.total < num_sms ? p.total : num_sms;
+    const long long tiles = (long long)p.B * p.tiles;
+    const long long grid = tiles < num_sms ? tiles : num_sms;
     return launch_pdl(kern, dim3((unsigned)grid), dim3(kAwThreads), ask, stream, mq, mk, p);
 }
 
@@ -501,9 +617,9 @@ cudaError_t launch_attn_weights(int B, int Lq, int Hq, int Hkv, int d, int Nc, i
     p.nht = (p.g + p.hpt - 1) / p.hpt;
     p.nblk = (Lq + p.tpt - 1) / p.tpt * p.nht;
     p.NB = (p.hpt * p.tpt + 15) / 16 * 16;
-    const int tiles = ((idx ? K : Nc) + kAwBM - 1) / kAwBM;
-    p.pairs = (tiles + 1) / 2;
-    p.total = (long long)B * p.pairs;
+    p.tiles = ((idx ? K : Nc) + kAwBM - 1) / kAwBM;
+    // (with idx every sequence has the same number of tiles: shares are even as they are)
+    p.counted = !idx && B <= kAwCounted && (long long)B * Lq <= kAwPositions && (long long)B * p.tiles < (1LL << 31);
     p.accumulate = accumulate;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.q_pos = q_pos;

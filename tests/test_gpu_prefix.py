@@ -220,3 +220,24 @@ def test_streams_capture_and_repeat(hb):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert hb.hyb_get_device_status() == hb.HYB_OK
+
+
+def test_wait_timeout_is_reported_and_the_device_recovers(hb):
+    # every wait inside the kernel is bounded: with a bound of 1 ns the first one
+    # that is not already satisfied runs out, and the call still returns
+    for shape in ((9, 1, 64, 1, 128, 4, 128, 700, 90), (3, 1, 4, 1, 64, 4, 128, 700, 90)):
+        c, q_pos, kv0, Lkv = _case(*shape)
+        ref, _ = _run(hb, c, q_pos, kv0, Lkv, 4, 128)
+        x = {n: t.cuda() for n, t in c.items()}
+        B, _, Hq, Hkv, d = shape[:5]
+        p = hb.problem(B=B, Lq=1, Lkv=Lkv, Hq=Hq, Hkv=Hkv, d=d, m=4, W=128, Nc=90,
+                       q_pos=torch.from_numpy(q_pos).cuda(), kv_pos0=torch.from_numpy(kv0).cuda())
+        hb.hyb_set_wait_limit_ns(1)
+        try:
+            hb.hyb_prefix_attn_fwd(p, *(x[n] for n in ("q", "kp", "vp", "kc", "vc", "k_raw", "v_raw")))
+            torch.cuda.synchronize()
+        finally:
+            hb.hyb_set_wait_limit_ns(0)
+        assert hb.hyb_get_device_status() == hb.HYB_ERR_DEVICE_TIMEOUT
+        again, _ = _run(hb, c, q_pos, kv0, Lkv, 4, 128)
+        assert torch.equal(ref, again)

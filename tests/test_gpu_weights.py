@@ -168,3 +168,28 @@ def test_streams_and_capture(hb, K):
         torch.cuda.synchronize()
         assert torch.equal(acc, 2 * want)
     assert hb.hyb_get_device_status() == hb.HYB_OK
+
+
+def test_many_sequences_and_many_positions(hb):
+    # more sequences, or more query positions, than a CTA counts at its start
+    for B, Lq, Nc in ((1100, 1, 140), (9, 1000, 150)):
+        q, kc, lse, _, q_pos = _case(B, Lq, 2, 1, 64, 4, 16, Nc)
+        if Lq > 1:
+            q_pos = np.array([[(b * 67 + t) % 700 for t in range(Lq)] for b in range(B)], np.int32)
+        acc = torch.full((B, Nc), float("nan"), device="cuda")
+        got = _call(hb, q, kc, lse, None, q_pos, 4, 16, acc=acc, accumulate=False)
+        _check(got, q, kc, lse, None, q_pos, 4, 16)
+
+
+def test_wait_timeout_is_reported_and_the_device_recovers(hb):
+    q, kc, lse, _, q_pos = _case(4, 1, 64, 1, 128, 4, 128, 3000)
+    ref = _call(hb, q, kc, lse, None, q_pos, 4, 128)
+    assert hb.hyb_get_device_status() == hb.HYB_OK
+    hb.hyb_set_wait_limit_ns(1)
+    try:
+        _call(hb, q, kc, lse, None, q_pos, 4, 128)
+    finally:
+        hb.hyb_set_wait_limit_ns(0)
+    assert hb.hyb_get_device_status() == hb.HYB_ERR_DEVICE_TIMEOUT
+    again = _call(hb, q, kc, lse, None, q_pos, 4, 128)
+    assert hb.hyb_get_device_status() == hb.HYB_OK and torch.equal(ref, again)
