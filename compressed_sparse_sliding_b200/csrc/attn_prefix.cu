@@ -62,34 +62,33 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t addr, uint32_t parity)
 
 // Bounded wait that tries the barrier some times before it looks at the clock
 // and the limit (a load from global memory, several hundred clocks): the waits
-// of these kernels are short and many.  Gives up when the CTA's abort flag is
-// up, like mbar_wait, which takes over afterwards; `tries` is wait_tries().
+// of these kernels are short and many, and their code is kept short (a role's loop
+// runs once a tile, so what it fetches counts).  Gives up when the CTA's abort flag
+// is up, or the limit expires (which raises it); `tries` is wait_tries().
 __device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int tries)
 {
     const uint32_t addr = smem_u32(bar);
+    if (mbar_test_wait(addr, parity))
+        return true;
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int it = 0; it < tries; ++it) {
-        if (mbar_try_wait(addr, parity))
+    for (int it = 0;; ++it) {
+        // (a try may sleep past a shortened limit)
+        if (tries ? mbar_try_wait(addr, parity) : mbar_test_wait(addr, parity))
             return true;
         if (*abort_flag)
             return false;
-    }
-    if (tries == 0 && !mbar_test_wait(addr, parity)) {
-        // a shortened limit: felt at once, also by waits that a try would sleep through
-        const uint64_t t0 = global_ns();
-        const uint64_t lim = *reinterpret_cast<volatile uint64_t *>(&g_wait_limit_ns);
-        while (!mbar_test_wait(addr, parity)) {
-            if (*abort_flag)
-                return false;
-            if (global_ns() - t0 > lim) {
-                set_error(HYB_ERR_DEVICE_TIMEOUT);
-                *abort_flag = 1;
-                return false;
-            }
+        if (it < tries)
+            continue;
+        const uint64_t t = global_ns();
+        if (t0 == 0)
+            t0 = t;
+        if (t - t0 > *reinterpret_cast<volatile uint64_t *>(&g_wait_limit_ns) || timed_out_somewhere()) {
+            set_error(HYB_ERR_DEVICE_TIMEOUT);
+            *abort_flag = 1;
+            return false;
         }
-        return true;
     }
-    return mbar_wait(bar, parity, abort_flag);
 }
 
 // None where the limit has been shortened.
@@ -497,7 +496,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         const int x = warp - 17;
         const uint32_t idesc_qk = idesc_bf16(kPfBM, kPfBN, false, false);
         const uint32_t idesc_pv = idesc_bf16(kPfBM, D, false, true);
-        const uint32_t aK = smem_u32(sK), aV = smem_u32(sV);
+        const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);                 // K-major
+        const uint64_t dV = sw128_desc(smem_u32(sV), kPfBN * 128, 1024);         // MN-major
         const uint32_t tS = tmem + x * kPfBN, tO = tmem + TM_O + x * 128;
         const bool leader = elect_one();
         uint32_t base = 0;            // key tiles of the items before this one
@@ -508,7 +508,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             release(nq);
             // this warp's key tiles: all of a pair's, or every second one
             const int step = it.pair ? 1 : 2, first = it.pair ? (x <= it.val1 ? 0 : it.nt) : x;
-            const uint32_t aQ = smem_u32(sQ) + (it.pair ? x : 0) * SM::Q_BYTES;
+            const uint64_t dq = sw128_desc(smem_u32(sQ) + (it.pair ? x : 0) * SM::Q_BYTES, 16, 1024);
             if (!(ok = wait(PB_QF, nq & 1)))
                 break;
             // O is free once the epilogue of this warp's previous item with keys has
@@ -540,11 +540,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                     ++pcnt;
                     tc_fence_after();
                     if (leader) {
+                        // (addresses are the low bits of a descriptor, in 16-byte units)
+                        const uint64_t dv = dV + (vs * SM::KV_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kPfBN / 16; ++kk) {
-                            const uint64_t db = sw128_desc(aV + vs * SM::KV_BYTES + kk * 16 * 128, kPfBN * 128, 1024);
                             // P of keys 64 .. 127 starts at column 64
-                            mma_bf16_ts(tO, tS + (kk >> 2) * 64 + (kk & 3) * 8, db, idesc_pv,
+                            mma_bf16_ts(tO, tS + (kk >> 2) * 64 + (kk & 3) * 8, dv + kk * 128, idesc_pv,
                                         (t == first + step && kk == 0) ? 0u : 1u);
                         }
                         mma_commit(&bar[PB_VE + vs]);
@@ -558,13 +559,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                         break;
                     tc_fence_after();
                     if (leader) {
+                        const uint64_t dk = dK + (ks * SM::KV_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t da = sw128_desc(aQ + (kk >> 2) * kPfBM * 128 + (kk & 3) * 32, 16, 1024);
-                            const uint64_t db = sw128_desc(aK + ks * SM::KV_BYTES + (kk >> 2) * kPfBN * 128 +
-                                                               (kk & 3) * 32,
-                                                           16, 1024);
-                            mma_bf16_ss(tS, da, db, idesc_qk, kk > 0 ? 1u : 0u);
+                            mma_bf16_ss(tS, dq + (kk >> 2) * (kPfBM * 8) + (kk & 3) * 2,
+                                        dk + (kk >> 2) * (kPfBN * 8) + (kk & 3) * 2, idesc_qk, kk > 0 ? 1u : 0u);
                         }
                         mma_commit(&bar[PB_SF + x]);
                         mma_commit(&bar[PB_KE + ks]);

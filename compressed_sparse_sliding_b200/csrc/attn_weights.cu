@@ -11,25 +11,28 @@
 // HBM bounds it, with many (the last tokens of a prompt) the exponentials.
 //
 // Layout.  S^T = K Q^T on tcgen05: keys are the MMA's M, so a TMEM lane is a key
-// and the sum over query rows stays inside one thread but for the two epilogue
-// warpgroups, which take alternate 32-row column chunks of S^T and add their two
-// sums through shared memory.  No atomics between CTAs: each entry has one owner,
-// and equal calls give equal bits.  A CTA owns a run of key tiles of one or more
+// and the sum over query rows stays inside one thread.  Four epilogue warpgroups
+// take key tiles in turn where a CTA has many (with two, each tile's chain of
+// barrier, TMEM load and exponentials was what the copies waited for: 57 us where
+// four take 44), and otherwise share every tile: every fourth 32-row column chunk,
+// the sums added through shared memory.  No atomics between CTAs: each entry has
+// one owner, and equal calls give equal bits.  A CTA owns a run of key tiles of one or more
 // sequences, every CTA the same number of tiles that hold visible entries.  Four
 // K stages and four S buffers (4 x 128 TMEM columns) keep copies, MMAs and
 // exponentials of different tiles running together.  Query blocks (hpt heads x
 // tpt tokens, up to 128 rows) stay in shared memory for the whole run where all
 // of a sequence's fit 64 KB (decode), and stream through the same slots otherwise.
 //
-// Roles (512 threads): warps 0-3 / 4-7 epilogue (thread = key, even / odd chunks),
-// warp 8 TMA producer, warp 9 MMA issue, warp 10 writes each query block's lse
-// and visible counts beside it, warps 12-15 gather the selected rows with
-// cp.async when idx is given (16 lanes per row).
+// Roles (768 threads): warps 0-15 epilogue (thread = key), warp 16 TMA producer,
+// warp 17 MMA issue, warps 18 and 19 write the query blocks' lse and visible counts
+// beside them (even and odd slots), warps 20-23 gather the selected rows with cp.async when idx is given
+// (16 lanes per row).
 #include "common.cuh"
 
 namespace hyb {
 
-constexpr int kAwThreads = 512;
+constexpr int kAwThreads = 768;
+constexpr int kAwWgs = 4;           // epilogue warpgroups
 constexpr int kAwBM = 128;          // keys of a tile
 constexpr int kAwKStages = 4;
 constexpr int kAwSBufs = 4;
@@ -43,7 +46,8 @@ constexpr int kAwZero = 4096;       // entries zeroed at a time
 
 struct WeightParams {
     int B, Lq, Hq, Hkv, g, Nc, m, W, e0, K;
-    int hpt, tpt, nht, nblk;        // heads and tokens of a query block, head tiles, blocks per KV head
+    int hpt, tpt, nht, ntt;         // heads and tokens of a query block; head and token tiles of a KV head
+    int split;                      // 1: the epilogue warpgroups share a tile's columns; 0: take alternate tiles
     int NB;                         // MMA columns of a block (rows rounded up to 16)
     int nqs, resident;              // query slots; all blocks of a sequence fit them
     int tiles;                      // key tiles of a full cache (idx: of the selection)
@@ -63,8 +67,9 @@ struct WeightSmem {
     static constexpr int OFF_K = kAwQBytes;
     static constexpr int OFF_COL = OFF_K + kAwKStages * K_BYTES;     // -lse (log2) per column, then counts
     static constexpr int NCOL = kAwQBytes / (D * 2);                 // columns of all slots together
-    static constexpr int OFF_SUM = OFF_COL + NCOL * 8;               // [2][128] sums of the second warpgroup
-    static constexpr int OFF_NV = OFF_SUM + 2 * kAwBM * 4;           // [kAwCounted] visible entries
+    static constexpr int OFF_SUM = OFF_COL + NCOL * 8;               // [2][3][128] sums of the other warpgroups
+    static constexpr int OFF_NV = OFF_SUM + 2 * (kAwWgs - 1) * kAwBM * 4;
+             // [kAwCounted] visible entries
     static constexpr int OFF_CUM = OFF_NV + kAwCounted * 4;          // [kAwCounted + 1] visible tiles before
     static constexpr int OFF_BAR = OFF_CUM + (kAwCounted + 4) * 4;
     static constexpr int OFF_MISC = OFF_BAR + 64 * 8;
@@ -105,8 +110,13 @@ struct WeightWalk {
         : b(0), nvs(nv_), cum(cum_)
     {
         const long long total = p.counted ? cum[p.B] : (long long)p.B * p.tiles;
-        u = total * blockIdx.x / gridDim.x;
-        end = total * (blockIdx.x + 1) / gridDim.x;
+        if (total < (1 << 20)) {       // (a 64-bit division is a hundred instructions)
+            u = (unsigned)total * blockIdx.x / gridDim.x;
+            end = (unsigned)total * (blockIdx.x + 1) / gridDim.x;
+        } else {
+            u = total * blockIdx.x / gridDim.x;
+            end = total * (blockIdx.x + 1) / gridDim.x;
+        }
         if (p.counted && u < end) {
             // the sequence of tile u: the last one with cum <= u
             int lo = 0, hi = p.B - 1;
@@ -137,14 +147,19 @@ struct WeightWalk {
             return true;
         }
         // shares of full caches: a sequence's visible tiles are spread over its share
-        r.b = (int)(u / p.tiles);
-        const int a0 = (int)(u % p.tiles);
+        r.b = u < (1ll << 31) ? (int)((unsigned)u / (unsigned)p.tiles) : (int)(u / p.tiles);
+        const int a0 = (int)(u - (long long)r.b * p.tiles);
         const int a1 = (int)min((long long)p.tiles, a0 + (end - u));
         u += a1 - a0;
         int nv = 0;
         for (int t = lane; t < p.Lq; t += 32)
             nv = max(nv, aw_visible(p, r.b * p.Lq + t));
         r.nv = __reduce_max_sync(0xffffffffu, nv);
+        if (p.idx) {                   // as many tiles as a full selection
+            r.lo = a0;
+            r.hi = a1;
+            return true;
+        }
         const long long T = aw_tiles(p, r.nv);
         r.lo = (int)(T * a0 / p.tiles);
         r.hi = (int)(T * a1 / p.tiles);
@@ -155,6 +170,22 @@ struct WeightWalk {
         return true;
     }
 };
+
+// S buffer of block i of a CTA's nt-th tile, and how often it was used before: a
+// warpgroup's own buffer, or the four in turn.
+__device__ __forceinline__ void aw_buffer(const WeightParams &p, uint32_t nt, int nblocks, int i, uint32_t &buf,
+                                          uint32_t &round)
+{
+    static_assert(kAwSBufs == kAwWgs, "a buffer a warpgroup");
+    if (p.split) {
+        const uint32_t n = nt * nblocks + i;
+        buf = n % kAwSBufs;
+        round = n / kAwSBufs;
+    } else {
+        buf = nt % kAwWgs;
+        round = nt / kAwWgs * nblocks + i;
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kAwThreads, 1)
@@ -182,8 +213,8 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kAwQStages; ++s) {
-            mbar_init(&bar[WB_QF + s], 1 + 32);    // the TMA copy, warp 10's lanes
-            mbar_init(&bar[WB_QE + s], 1 + 8);     // the MMA, the epilogue warps
+            mbar_init(&bar[WB_QF + s], 1 + 32);    // the TMA copy, the lanes of warp 18 or 19
+            mbar_init(&bar[WB_QE + s], 1 + 4 * kAwWgs);   // the MMA, the epilogue warps
         }
         for (int s = 0; s < kAwKStages; ++s) {
             mbar_init(&bar[WB_KF + s], p.idx ? 128 : 1);
@@ -191,10 +222,10 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         for (int s = 0; s < kAwSBufs; ++s) {
             mbar_init(&bar[WB_SF + s], 1);
-            mbar_init(&bar[WB_SE + s], 8);
+            mbar_init(&bar[WB_SE + s], p.split ? 4 * kAwWgs : 4);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar[WB_TF + s], 4);         // the second warpgroup's sums
+            mbar_init(&bar[WB_TF + s], 4 * (kAwWgs - 1));   // the other warpgroups' sums
             mbar_init(&bar[WB_TE + s], 4);
         }
         mbar_init(&bar[WB_DONE], 1);
@@ -203,7 +234,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
     for (int b = threadIdx.x; p.counted && b < p.B; b += kAwThreads)
         sSeq[b] = 0;
-    if (warp == 9)
+    if (warp == 17)
         tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), 512);
     tc_fence_before();
     __syncthreads();
@@ -242,30 +273,46 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
 
     const uint32_t qbytes = (uint32_t)p.NB * D * 2;
-    const int nblocks = p.Hkv * p.nblk;            // query blocks of a sequence
-    // Query slot and fill count of the n-th block use: with resident blocks a
-    // slot is filled once a run, otherwise the blocks go round the slots.
+    const int nblocks = p.Hkv * p.ntt * p.nht;     // query blocks of a sequence
     auto wait = [&](int b, uint32_t parity) {      // whole warp
         return __all_sync(0xffffffffu, mbar_wait_short(&bar[b], parity, abort_flag, tries)) != 0;
     };
     WeightWalk walk(p, sSeq, sCum);
     WeightRun r;
     bool ok = true;
+    uint32_t runs = 0;                             // runs with tiles so far
+    // Query slots go round (streamed blocks): the next use's slot, and its fill's parity.
+    uint32_t ring = 0, ring_par = 0;
+    auto advance = [&]() {
+        if (++ring == (uint32_t)p.nqs) {
+            ring = 0;
+            ring_par ^= 1;
+        }
+    };
+    // The blocks of a sequence, by KV head, token tile and head tile (no divisions:
+    // they would cost more than a block's other instructions).
+    auto for_blocks = [&](auto f) {
+        int i = 0;
+        for (int h = 0; ok && h < p.Hkv; ++h)
+            for (int tt = 0; ok && tt < p.ntt; ++tt)
+                for (int ht = 0; ok && ht < p.nht; ++ht, ++i)
+                    f(i, h, tt * p.tpt, ht * p.hpt, tt + ht == 0, tt == p.ntt - 1 && ht == p.nht - 1);
+    };
 
-    if (warp == 8 || warp == 10) {
-        // ============ query blocks: copies (warp 8), lse and counts (warp 10); K tiles (warp 8) ============
-        uint32_t kc = 0, qc = 0, runs = 0;
+    if (warp == 16 || warp == 18 || warp == 19) {
+        // ============ query blocks: copies (warp 16), lse and counts (warps 18, 19); K tiles (warp 16) ============
+        uint32_t kc = 0, qc = 0;
         const uint32_t box_bytes = (uint32_t)p.hpt * p.tpt * D * 2;
         while (ok && walk.next(p, lane, r)) {
             for (int tile = r.lo; ok && tile < r.hi; ++tile) {
-                for (int i = 0; ok && i < nblocks; ++i) {
-                    const int h = i / p.nblk, blk = i - h * p.nblk;
-                    const bool load_k = warp == 8 && blk == 0 && !p.idx;
-                    const bool load_q = !p.resident || tile == r.lo;
-                    if (load_k) {
+                const bool load_q = !p.resident || tile == r.lo;
+                if (!load_q && (warp >= 18 || p.idx))
+                    break;
+                for_blocks([&](int i, int h, int t0, int h0, bool first, bool) {
+                    if (warp == 16 && first && !p.idx) {
                         const uint32_t st = kc % kAwKStages;
                         if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
-                            break;
+                            return;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&bar[WB_KF + st], SM::K_BYTES);
                             for (int cb = 0; cb < NCB; ++cb)
@@ -276,12 +323,17 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         ++kc;
                     }
                     if (!load_q)
-                        continue;
-                    const uint32_t st = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
-                    const int t0 = (blk / p.nht) * p.tpt, h0 = (blk % p.nht) * p.hpt;
-                    if (warp == 8) {
-                        if (fill > 0 && !(ok = wait(WB_QE + st, (fill - 1) & 1)))
-                            break;
+                        return;
+                    const uint32_t st = p.resident ? i : ring, par = p.resident ? runs & 1 : ring_par;
+                    const bool used = p.resident ? runs > 0 : qc >= (uint32_t)p.nqs;
+                    if (warp >= 18 && (st & 1) != (uint32_t)(warp - 18)) {
+                        ++qc;              // the other warp's slot
+                        advance();
+                        return;
+                    }
+                    if (warp == 16) {
+                        if (used && !(ok = wait(WB_QE + st, par ^ 1)))
+                            return;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&bar[WB_QF + st], box_bytes);
                             for (int cb = 0; cb < NCB; ++cb)
@@ -296,18 +348,20 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int c = lane + 32 * k;
-                            const int t = t0 + c / p.hpt, hd = h0 + c % p.hpt;
                             l[k] = 0.f;
                             nv[k] = 0;
-                            if (c < p.hpt * p.tpt && t < p.Lq && hd < p.g) {
-                                l[k] = p.lse[((size_t)r.b * p.Hq + h * p.g + hd) * p.Lq + t];
-                                nv[k] = p.Lq == 1 ? r.nv : aw_visible(p, r.b * p.Lq + t);
-                                least = min(least, nv[k]);
+                            if (c < p.hpt * p.tpt) {
+                                const int dt = c / p.hpt, t = t0 + dt, hd = h0 + c - dt * p.hpt;
+                                if (t < p.Lq && hd < p.g) {
+                                    l[k] = p.lse[((size_t)r.b * p.Hq + h * p.g + hd) * p.Lq + t];
+                                    nv[k] = p.Lq == 1 ? r.nv : aw_visible(p, r.b * p.Lq + t);
+                                    least = min(least, nv[k]);
+                                }
                             }
                         }
                         least = __reduce_min_sync(0xffffffffu, least);
-                        if (fill > 0 && !(ok = wait(WB_QE + st, (fill - 1) & 1)))
-                            break;
+                        if (used && !(ok = wait(WB_QE + st, par ^ 1)))
+                            return;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int c = lane + 32 * k;
@@ -321,12 +375,13 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         mbar_arrive(&bar[WB_QF + st]);
                     }
                     ++qc;
-                }
+                    advance();
+                });
             }
             if (r.hi > r.lo)
                 ++runs;
         }
-        if (warp == 8 && lane == 0) {
+        if (warp == 16 && lane == 0) {
             // unwinding: wait for the last copies issued into every slot
             for (uint32_t c = (kc > kAwKStages ? kc - kAwKStages : 0); c < kc; ++c)
                 drain_wait(&bar[WB_KF + c % kAwKStages], (c / kAwKStages) & 1);
@@ -338,13 +393,13 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     drain_wait(&bar[WB_QF + c], ((qc - 1 - c) / nblocks) & 1);
             }
         }
-    } else if (warp >= 12) {
+    } else if (warp >= 20) {
         // ============================ selected rows: gather ============================
         if (p.idx) {
             constexpr int CH = D / 8;              // 16-byte chunks of a row
             constexpr int RPI = 128 / CH;          // rows a pass
             constexpr int N = kAwBM / RPI;
-            const int pt = threadIdx.x - 12 * 32;
+            const int pt = threadIdx.x - 20 * 32;
             const int c8 = pt % CH, rsub = pt / CH;
             const uint32_t dchunk = (c8 >> 3) * kAwBM * 128;
             uint32_t kc = 0;
@@ -382,51 +437,48 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             cp_async_wait_group<0>();
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ================================ MMA issue ================================
         const uint32_t idesc = idesc_bf16(kAwBM, p.NB, false, false);
-        const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK);
-        uint32_t kc = 0, qc = 0, runs = 0, sc = 0;
+        const uint64_t dQ = sw128_desc(smem_u32(sQ), 16, 1024), dK = sw128_desc(smem_u32(sK), 16, 1024);
+        uint32_t kc = 0, nt = 0;
         const bool leader = elect_one();
         while (ok && walk.next(p, lane, r)) {
-            for (int tile = r.lo; ok && tile < r.hi; ++tile) {
-                for (int i = 0; ok && i < nblocks; ++i) {
-                    const int blk = i % p.nblk;
-                    const uint32_t qs = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
-                    const uint32_t ks = kc % kAwKStages, buf = sc % kAwSBufs;
-                    if (!(ok = wait(WB_QF + qs, fill & 1)))
-                        break;
-                    ++qc;
-                    if (blk == 0) {
+            for (int tile = r.lo; ok && tile < r.hi; ++tile, ++nt) {
+                for_blocks([&](int i, int, int, int, bool first, bool last) {
+                    const uint32_t qs = p.resident ? i : ring, par = p.resident ? runs & 1 : ring_par;
+                    const uint32_t ks = kc % kAwKStages;
+                    uint32_t buf, round;
+                    aw_buffer(p, nt, nblocks, i, buf, round);
+                    if (!(ok = wait(WB_QF + qs, par)))
+                        return;
+                    advance();
+                    if (first) {
                         if (!(ok = wait(WB_KF + ks, (kc / kAwKStages) & 1)))
-                            break;
+                            return;
                         if (p.idx)
                             fence_proxy_async_smem();   // rows written by cp.async, read by the MMA
                     }
-                    if (sc >= kAwSBufs && !(ok = wait(WB_SE + buf, ((sc / kAwSBufs) - 1) & 1)))
-                        break;
+                    if (round > 0 && !(ok = wait(WB_SE + buf, (round - 1) & 1)))
+                        return;
                     tc_fence_after();
                     if (leader) {
+                        // (addresses are the low bits of a descriptor, in 16-byte units)
+                        const uint64_t da = dK + (ks * SM::K_BYTES >> 4), db = dQ + (qs * qbytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t da = sw128_desc(aK + ks * SM::K_BYTES + (kk >> 2) * kAwBM * 128 +
-                                                               (kk & 3) * 32,
-                                                           16, 1024);
-                            const uint64_t db = sw128_desc(aQ + qs * qbytes + (kk >> 2) * p.NB * 128 + (kk & 3) * 32,
-                                                           16, 1024);
-                            mma_bf16_ss(tmem + buf * 128, da, db, idesc, kk > 0 ? 1u : 0u);
+                            mma_bf16_ss(tmem + buf * 128, da + (kk >> 2) * (kAwBM * 8) + (kk & 3) * 2,
+                                        db + (kk >> 2) * (p.NB * 8) + (kk & 3) * 2, idesc, kk > 0 ? 1u : 0u);
                         }
                         mma_commit(&bar[WB_SF + buf]);
-                        if (blk == p.nblk - 1)
+                        if (last)
                             mma_commit(&bar[WB_KE + ks]);
                         if (!p.resident || tile == r.hi - 1)
                             mma_commit(&bar[WB_QE + qs]);
                     }
                     __syncwarp();
-                    ++sc;
-                    if (blk == p.nblk - 1)
-                        ++kc;
-                }
+                    kc += last;
+                });
             }
             if (r.hi > r.lo)
                 ++runs;
@@ -435,46 +487,50 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             mma_commit(&bar[WB_DONE]);
         __syncwarp();
         drain_wait(&bar[WB_DONE], 0);
-    } else if (warp < 8) {
+    } else if (warp < 4 * kAwWgs) {
         // ============================ exponentials and sums ============================
         const int x = warp >> 2;
         const int quad = warp & 3;
         const int key = quad * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        uint32_t qc = 0, runs = 0, sc = 0, tc = 0;
+        uint32_t nt = 0;                    // tiles so far
         if (p.counted && !p.accumulate && !p.idx) {
             // entries that no query token sees
             const int per = (p.Nc + kAwZero - 1) / kAwZero;
             for (int w = blockIdx.x; w < p.B * per; w += gridDim.x) {
                 const int b = w / per, c = (w - b * per) * kAwZero, end = min(p.Nc, c + kAwZero);
-                for (int j = max(sSeq[b], c) + (int)threadIdx.x; j < end; j += 256)
+                for (int j = max(sSeq[b], c) + (int)threadIdx.x; j < end; j += 128 * kAwWgs)
                     p.acc[(size_t)b * p.Nc + j] = 0.f;
             }
         }
         while (ok && walk.next(p, lane, r)) {
-            for (int j = r.z0 + (int)threadIdx.x; j < r.z1; j += 256)
+            for (int j = r.z0 + (int)threadIdx.x; j < r.z1; j += 128 * kAwWgs)
                 p.acc[(size_t)r.b * p.Nc + j] = 0.f;
-            for (int tile = r.lo; ok && tile < r.hi; ++tile) {
+            for (int tile = r.lo; ok && tile < r.hi; ++tile, ++nt) {
+                if (!p.split && (int)(nt % kAwWgs) != x)
+                    continue;                            // another warpgroup's
                 const int j = tile * kAwBM + key;        // entry, or slot of the selection
+                int e = -1;
+                if (p.idx && (!p.split || x == 0) && j < p.K)
+                    e = __ldg(p.idx + (size_t)r.b * p.K + j);
                 float tot = 0.f;
-                for (int i = 0; ok && i < nblocks; ++i) {
-                    const int blk = i % p.nblk;
-                    const uint32_t qs = p.resident ? i : qc % p.nqs, fill = p.resident ? runs : qc / p.nqs;
-                    const uint32_t buf = sc % kAwSBufs;
-                    ++qc;
-                    if (!(ok = wait(WB_QF + qs, fill & 1) && wait(WB_SF + buf, (sc / kAwSBufs) & 1)))
-                        break;
+                for_blocks([&](int i, int, int t0, int h0, bool, bool) {
+                    const uint32_t qs = p.resident ? i : ring, par = p.resident ? runs & 1 : ring_par;
+                    uint32_t buf, round;
+                    aw_buffer(p, nt, nblocks, i, buf, round);
+                    if (!(ok = wait(WB_QF + qs, par) && wait(WB_SF + buf, round & 1)))
+                        return;
+                    advance();
                     tc_fence_after();
                     // rows of this block: whole tokens, or the heads of a group's last tile
-                    const int t0 = (blk / p.nht) * p.tpt, h0 = (blk % p.nht) * p.hpt;
                     const int ncv = min(p.hpt, p.g - h0) * min(p.tpt, p.Lq - t0);
                     const bool full = p.idx || (tile + 1) * kAwBM <= sMin[qs];
                     const uint32_t tS = tl + buf * 128;
                     const float *nl = sLse + qs * p.NB;
                     const int *cn = sNv + qs * p.NB;
 #pragma unroll 1
-                    for (int c = 32 * x; c < ncv; c += 64) {
+                    for (int c = p.split ? 32 * x : 0; c < ncv; c += p.split ? 32 * kAwWgs : 32) {
                         float sv[32];
                         tmem_ld32(tS + c, sv);
                         tmem_ld_wait();
@@ -509,40 +565,51 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&bar[WB_SE + buf]);
-                        if (!p.resident || tile == r.hi - 1)
+                        if (!p.resident)
                             mbar_arrive(&bar[WB_QE + qs]);   // this warp has read the slot's columns
                     }
-                    ++sc;
-                }
+                });
                 if (!ok)
                     break;
-                // the two warpgroups' sums meet
-                const uint32_t tb = tc & 1;
-                if (x == 1) {
-                    if (tc >= 2 && !(ok = wait(WB_TE + tb, ((tc >> 1) - 1) & 1)))
+                if (p.split) {
+                    // the warpgroups' sums meet
+                    const uint32_t tb = nt & 1, round = nt >> 1;
+                    float *sums = sSum + tb * (kAwWgs - 1) * kAwBM + key;
+                    if (x > 0) {
+                        if (round > 0 && !(ok = wait(WB_TE + tb, (round - 1) & 1)))
+                            break;
+                        sums[(x - 1) * kAwBM] = tot;
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&bar[WB_TF + tb]);
+                        continue;
+                    }
+                    if (!(ok = wait(WB_TF + tb, round & 1)))
                         break;
-                    sSum[tb * kAwBM + key] = tot;
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&bar[WB_TF + tb]);
-                } else {
-                    if (!(ok = wait(WB_TF + tb, (tc >> 1) & 1)))
-                        break;
-                    tot += sSum[tb * kAwBM + key];
+#pragma unroll
+                    for (int k = 0; k < kAwWgs - 1; ++k)
+                        tot += sums[k * kAwBM];
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&bar[WB_TE + tb]);
-                    if (p.idx) {
-                        const int e = j < p.K ? p.idx[(size_t)r.b * p.K + j] : -1;
-                        // an entry listed twice counts twice, whichever is added first
-                        if (e >= 0 && e < r.nv)
-                            atomicAdd(&p.acc[(size_t)r.b * p.Nc + e], tot);
-                    } else if (j < r.nv) {
-                        float *a = &p.acc[(size_t)r.b * p.Nc + j];
-                        *a = p.accumulate ? *a + tot : tot;
-                    }
                 }
-                ++tc;
+                if (p.idx) {
+                    // an entry listed twice counts twice, whichever is added first
+                    if (e >= 0 && e < r.nv)
+                        atomicAdd(&p.acc[(size_t)r.b * p.Nc + e], tot);
+                } else if (j < r.nv) {
+                    float *a = &p.acc[(size_t)r.b * p.Nc + j];
+                    *a = p.accumulate ? *a + tot : tot;
+                }
+            }
+            if (ok && p.resident && r.hi > r.lo) {
+                // this warp has read the run's columns (it waits for them even where it
+                // had no tile of the run, so that it never releases a slot a run ahead)
+                for (int i = 0; ok && i < nblocks; ++i) {
+                    ok = wait(WB_QF + i, runs & 1);
+                    if (ok && lane == 0)
+                        mbar_arrive(&bar[WB_QE + i]);
+                }
             }
             if (r.hi > r.lo)
                 ++runs;
@@ -551,7 +618,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc((uint32_t)misc[0], 512);
     }
@@ -573,7 +640,8 @@ static cudaError_t launch_weights_t(WeightParams &p, const void *q, const void *
     p.nqs = kAwQBytes / (p.NB * D * 2);
     if (p.nqs > kAwQStages)
         p.nqs = kAwQStages;
-    p.resident = (long long)p.Hkv * p.nblk <= p.nqs;
+    p.resident = (long long)p.Hkv * p.ntt * p.nht <= p.nqs;
+    p.split = !p.resident || (long long)p.B * p.tiles < 2LL * num_sms;
     CUtensorMap mq, mk;
     if (!make_map(&mq, q, D, p.Hq, p.Lq, p.B, p.hpt, p.tpt) ||
         !make_map(&mk, kc, D, p.Hkv, p.Nc, p.B, 1, kAwBM))
@@ -615,7 +683,7 @@ cudaError_t launch_attn_weights(int B, int Lq, int Hq, int Hkv, int d, int Nc, i
     p.hpt = p.g < 128 ? p.g : 128;
     p.tpt = 128 / p.hpt < Lq ? 128 / p.hpt : Lq;
     p.nht = (p.g + p.hpt - 1) / p.hpt;
-    p.nblk = (Lq + p.tpt - 1) / p.tpt * p.nht;
+    p.ntt = (Lq + p.tpt - 1) / p.tpt;
     p.NB = (p.hpt * p.tpt + 15) / 16 * 16;
     p.tiles = ((idx ? K : Nc) + kAwBM - 1) / kAwBM;
     // (with idx every sequence has the same number of tiles: shares are even as they are)
