@@ -18,7 +18,12 @@
 //              tiles are fetched once for 256 rows);
 //   alternate  where there is a single query tile, the two softmax warpgroups
 //              take its even and odd key tiles, each with its own maximum, sum
-//              and O, and store two parts (HBM-bound: twice the tiles in flight).
+//              and O (HBM-bound: twice the tiles in flight), and join them in
+//              TMEM: every warp can read both O's of its lanes.
+// Where a sequence's own query rows fill the tiles (chunks of a prompt), or the
+// prefix is short, the shared entries are not taken apart: an item's stream then is
+// prefix, own entries, window, and if no item is cut the kernel writes o itself, with
+// no parts and no second kernel.  prefix_plan takes whichever way it reckons faster.
 // A query tile holds hpt heads of one KV group x tpt tokens (hpt = min(g, 128),
 // tpt = 128 / hpt), fetched by one TMA box; rows past hpt * tpt are not used.
 //
@@ -117,7 +122,6 @@ constexpr int kPfPolyPairs = 2;       // of eight pairs of exponentials
 // The split is planned for this many SMs on every device, so that the workspace
 // size is a function of the problem alone.
 constexpr int kPfPlanSMs = 148;
-constexpr int kPfPairCost = 17, kPfAltCost = 8, kPfItemCost = 20;    // 1/8 us, see prefix_plan
 
 struct PrefixParams {
     int B, Lq, Lkv, Hq, Hkv, g, Np, Nc, m, W;
@@ -132,6 +136,7 @@ struct PrefixParams {
     int o_len, o_over, o_rem, o_a, o_b, o_total;
     int ctas, ctas_used;          // planned for, and with work
     int p_parts, n_parts;         // partial results per row: of the shared entries, in all (upper bound)
+    int merged, direct;           // own items go through the shared entries too; and write o themselves
     long long rows;               // B * Lq * Hq
     float scale_log2;
     const int32_t *q_pos, *kv_pos0;
@@ -171,17 +176,30 @@ struct PrefixItem {
     int tok0[2], h0[2];  // first token (of the batch's B * Lq, or of the sequence) and head of each query tile
     int val1;            // the second query tile exists (pair)
     int ntok;            // tokens of the range tok0 counts in
-    int nent;            // entries that some row of the item sees
+    int npre, nent;      // shared and own entries that some row of the item sees
     int rlo, nraw;       // first raw row and number of raw rows that some row sees
-    int nte;             // entry tiles before the raw tiles
+    int ntp, nte;        // tiles: shared entries, own entries (then raw rows)
     int t0, nt;          // first key tile and number of key tiles of this piece
 };
 
 // What one token of an item sees.
 struct PrefixToken {
-    int nv;              // entries
+    int nv;              // entries, shared and own
     int wlo, whi;        // raw rows
 };
+
+// Key tile t of an item: 0 shared entries, 1 own entries, 2 raw rows; and its number
+// among its kind.
+__device__ __forceinline__ int pf_kind(const PrefixItem &it, int &t)
+{
+    if (t < it.ntp)
+        return 0;
+    t -= it.ntp;
+    if (t < it.nte)
+        return 1;
+    t -= it.nte;
+    return 2;
+}
 
 template <int D>
 struct PrefixSmem {
@@ -192,7 +210,7 @@ struct PrefixSmem {
     static constexpr int OFF_K = 2 * Q_BYTES;
     static constexpr int OFF_V = OFF_K + kPfStages * KV_BYTES;
     static constexpr int OFF_ST = OFF_V + kPfStages * KV_BYTES;
-    static constexpr int OFF_MAX = OFF_ST + 16 * STAGE_BYTES;          // per softmax thread: maximum, then sum
+    static constexpr int OFF_MAX = OFF_ST + 16 * STAGE_BYTES;          // per softmax thread: a tile's maximum
     static constexpr int OFF_TOK = OFF_MAX + kPfSoftmaxThreads * 4;
     static constexpr int OFF_ITEM = OFF_TOK + kPfItemSlots * 256 * (int)sizeof(PrefixToken);
     static constexpr int OFF_BAR = (OFF_ITEM + kPfItemSlots * (int)sizeof(PrefixItem) + 15) / 16 * 16;
@@ -203,7 +221,7 @@ static_assert(1024 + PrefixSmem<128>::BYTES <= 227 * 1024, "shared memory of a C
 
 // barrier slots (two each from PB_KF on, three item slots)
 enum { PB_QF = 0, PB_QE = 1, PB_KF = 2, PB_KE = 4, PB_VF = 6, PB_VE = 8, PB_SF = 10, PB_PF = 12, PB_OF = 14,
-       PB_OE = 16, PB_IF = 18, PB_IE = 21, PB_DONE = 24, PB_MEET = 25 };
+       PB_OE = 16, PB_IF = 18, PB_IE = 21, PB_DONE = 24, PB_MEET = 25, PB_MEET4 = 33 };
 
 // Entries visible to position pos: those ending before its window.
 __device__ __forceinline__ int pf_visible(long long pos, int m, int W, int n)
@@ -250,7 +268,7 @@ __device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int
         u = i % p.p_units;
         it.kvh = i / p.p_units;
         it.b = 0;
-        it.part = it.pair ? s : 2 * s;
+        it.part = s;
         it.ntok = p.B * p.Lq;
     } else {
         it.pair = p.o_pair;
@@ -258,7 +276,7 @@ __device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int
         const int r = i / p.o_units;
         it.kvh = r % p.Hkv;
         it.b = r / p.Hkv;
-        it.part = p.p_parts + (it.pair ? s : 2 * s);
+        it.part = p.p_parts + s;
         it.ntok = p.Lq;
     }
     const long long kv0 = !pre && p.kv_pos0 ? p.kv_pos0[it.b] : 0;
@@ -278,8 +296,7 @@ __device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int
             if (it.tok0[x] + t < it.ntok) {
                 const int flat = (pre ? 0 : it.b * p.Lq) + it.tok0[x] + t;
                 const long long pos = p.q_pos ? p.q_pos[flat] : flat % p.Lq;
-                const int nv = pf_visible(pos, p.m, p.W, p.Np + p.Nc);
-                tk.nv = pre ? min(nv, p.Np) : max(nv - p.Np, 0);
+                tk.nv = pf_visible(pos, p.m, p.W, p.Np + p.Nc);
                 nmax = max(nmax, tk.nv);
                 if (!pre && p.W > 0) {
                     const long long lo = max(0ll, max(0ll, pos - p.W + 1) - kv0);
@@ -295,12 +312,15 @@ __device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int
             tokens[x * 128 + t] = tk;
         }
     }
-    it.nent = __reduce_max_sync(0xffffffffu, nmax);
+    nmax = __reduce_max_sync(0xffffffffu, nmax);
+    it.npre = pre || p.merged ? min(nmax, p.Np) : 0;
+    it.nent = pre ? 0 : max(nmax - p.Np, 0);
     it.rlo = __reduce_min_sync(0xffffffffu, rlo);
     rhi = __reduce_max_sync(0xffffffffu, rhi);
     it.nraw = rhi >= 0 ? rhi - it.rlo + 1 : 0;
+    it.ntp = (it.npre + kPfBN - 1) / kPfBN;
     it.nte = (it.nent + kPfBN - 1) / kPfBN;
-    const int T = it.nte + (it.nraw + kPfBN - 1) / kPfBN;
+    const int T = it.ntp + it.nte + (it.nraw + kPfBN - 1) / kPfBN;
     if (pre) {
         it.t0 = (int)((long long)T * s / p.p_ns);
         it.nt = (int)((long long)T * (s + 1) / p.p_ns) - it.t0;
@@ -347,7 +367,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             mbar_init(&bar[PB_SF + s], 1);
             mbar_init(&bar[PB_PF + s], 8);     // one arrival a warp
             mbar_init(&bar[PB_OF + s], 1);
-            mbar_init(&bar[PB_OE + s], 8);
+            mbar_init(&bar[PB_OE + s], 16);    // both warpgroups (alternate), or two from one
         }
         for (int s = 0; s < kPfItemSlots; ++s) {
             mbar_init(&bar[PB_IF + s], 1);
@@ -356,6 +376,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         mbar_init(&bar[PB_DONE], 2);
         for (int s = 0; s < 8; ++s)
             mbar_init(&bar[PB_MEET + s], 2);
+        for (int s = 0; s < 4; ++s)
+            mbar_init(&bar[PB_MEET4 + s], 4);
         mbar_fence_init();
         misc[1] = 0;
     }
@@ -448,11 +470,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                         uint8_t *ring = kv ? sV : sK;
                         uint64_t *full = &bar[kv ? PB_VF : PB_KF], *empty = &bar[kv ? PB_VE : PB_KE];
                         for (int j = i; j < min(i + per, it.nt); ++j) {
-                            const int t = it.t0 + j;
-                            const bool ent = t < it.nte;
-                            const int row0 = ent ? t * kPfBN : it.rlo + (t - it.nte) * kPfBN;
-                            const CUtensorMap *map = kv ? (!ent ? &tm_vr : it.pre ? &tm_vp : &tm_vc)
-                                                        : (!ent ? &tm_kr : it.pre ? &tm_kp : &tm_kc);
+                            int t = it.t0 + j;
+                            const int kind = pf_kind(it, t);
+                            const int row0 = (kind == 2 ? it.rlo : 0) + t * kPfBN;
+                            const CUtensorMap *map = kv ? (kind == 0 ? &tm_vp : kind == 1 ? &tm_vc : &tm_vr)
+                                                        : (kind == 0 ? &tm_kp : kind == 1 ? &tm_kc : &tm_kr);
                             const uint32_t st = cnt % kPfStages;
                             if (cnt >= kPfStages &&
                                 !mbar_wait_short(&empty[st], ((cnt / kPfStages) - 1) & 1, abort_flag, tries)) {
@@ -472,7 +494,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                             mbar_arrive_expect_tx(&full[st], SM::KV_BYTES);
                             for (int cb = 0; cb < NCB; ++cb)
                                 tma_load_4d(ring + st * SM::KV_BYTES + cb * kPfBN * 128, map, &full[st], cb * 64,
-                                            it.kvh, row0, it.b);
+                                            it.kvh, row0, kind == 0 ? 0 : it.b);
                             ++cnt;
                         }
                     }
@@ -520,8 +542,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                     const uint32_t n = base + t - step, vs = n % kPfStages;
                     if (!(ok = wait(PB_VF + vs, (n / kPfStages) & 1)))
                         break;
-                    const int kt = it.t0 + t - step;
-                    const int seen = kt < it.nte ? it.nent - kt * kPfBN : it.nraw - (kt - it.nte) * kPfBN;
+                    int kt = it.t0 + t - step;
+                    const int kind = pf_kind(it, kt);
+                    const int seen = (kind == 0 ? it.npre : kind == 1 ? it.nent : it.nraw) - kt * kPfBN;
                     if (seen < kPfBN) {
                         // rows that no query of the item sees take no part, whatever they hold
                         for (int cb = 0; cb < NCB; ++cb)
@@ -596,11 +619,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t tS = tl + x * kPfBN + half * 64;
         const uint32_t tO = tl + TM_O + x * 128 + half * (D / 2);
+        const uint32_t tOA = tl + TM_O;         // O of A; O of B is 128 columns on
         float *mine = reinterpret_cast<float *>(smem + SM::OFF_MAX) + threadIdx.x;
         const float *other = reinterpret_cast<float *>(smem + SM::OFF_MAX) + (threadIdx.x ^ 128);
         // the two warps of a row quad meet: bounded, like every wait (a named barrier
         // would keep one of them for ever if the other gave up)
-        uint32_t met = 0;
+        uint32_t met = 0, met4 = 0;
         auto meet = [&]() {
             __syncwarp();
             if (lane == 0)
@@ -620,7 +644,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             const int tok = (xt ? it.tok0[1] : it.tok0[0]) + rtok;
             const int h = (xt ? it.h0[1] : it.h0[0]) + rhead;
             const bool valid_row = rtok < p.tpt && tok < it.ntok && h < (it.kvh + 1) * p.g && xt <= it.val1;
-            PrefixToken tk = {0, 0, -1};
+            PrefixToken tk = {0, 0, -1};   // nothing visible
             if (valid_row)
                 tk = sTok[(nq % kPfItemSlots) * 256 + xt * 128 + rtok];
             release(nq);
@@ -635,14 +659,14 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 tc_fence_after();
                 if (warp_rows) {
                     // keys c_lo .. c_lo + c_n of this half of the tile are visible to this row
-                    int c_lo = 0, c_hi;
-                    const int kt = it.t0 + t;
-                    if (kt < it.nte) {
-                        c_hi = min(tk.nv - 1 - kt * kPfBN - half * 64, 63);
+                    int c_lo = 0, c_hi, kt = it.t0 + t;
+                    const int kind = pf_kind(it, kt);
+                    const int r0 = kt * kPfBN + half * 64;
+                    if (kind == 2) {
+                        c_lo = max(0, tk.wlo - it.rlo - r0);
+                        c_hi = min(tk.whi - it.rlo - r0, 63);
                     } else {
-                        const int r0 = it.rlo + (kt - it.nte) * kPfBN + half * 64;
-                        c_lo = max(0, tk.wlo - r0);
-                        c_hi = min(tk.whi - r0, 63);
+                        c_hi = min((kind == 0 ? min(tk.nv, p.Np) : tk.nv - p.Np) - 1 - r0, 63);
                     }
                     // (rows of no query go along with the others: nothing of theirs is kept)
                     const bool full = __all_sync(0xffffffffu, !valid_row || (c_lo == 0 && c_hi == 63));
@@ -755,70 +779,155 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 ++ocnt;
                 tc_fence_after();
             }
+            // The row's sum over both halves, and in an alternating item the two
+            // streams' maxima and sums: weights ws of this warpgroup's (pair) or of A's
+            // and B's O, maximum m_ref and sum l_sum of the result.
+            float ws[2] = {1.f, 0.f};
             if (warp_rows) {
-                *mine = l_sum;
-                if (!(ok = meet()))
-                    break;
-                l_sum += *other;
-                if (!(ok = meet()))      // before the next item's first maximum
-                    break;
-            }
-            const long long at = (long long)(it.part + (it.pair ? 0 : x)) * p.rows + (long long)flat * p.Hq + h;
-            if (valid_row && half == 0)
-                p.part_ml[at] = make_float2(m_ref, l_sum);
-            const unsigned stored = __ballot_sync(0xffffffffu, valid_row && l_sum != 0.f);
-            if (stored) {
-                float *orow = p.part_o + at * D + half * (D / 2);
-                if (__popc(stored) <= 8) {
-                    // few rows: each lane writes its own
-#pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 32) {
-                        float ov[32];
-                        tmem_ld32(tO + c, ov);
-                        tmem_ld_wait();
-                        if ((stored >> lane) & 1) {
-#pragma unroll
-                            for (int q = 0; q < 32; q += 4)
-                                *reinterpret_cast<float4 *>(orow + c + q) =
-                                    make_float4(ov[q], ov[q + 1], ov[q + 2], ov[q + 3]);
-                        }
-                    }
+                float2 *ml = reinterpret_cast<float2 *>(stage) + lane;
+                const float2 *of = reinterpret_cast<const float2 *>(stage + ((warp ^ 4) - warp) * SM::STAGE_BYTES) + lane;
+                const int hop = ((warp ^ 8) - warp) * SM::STAGE_BYTES / (int)sizeof(float2);
+                *ml = make_float2(m_ref, l_sum);
+                tc_fence_before();
+                if (it.pair) {
+                    if (!(ok = meet()))
+                        break;
+                    l_sum += of->y;
+                    if (!(ok = meet()))        // before the stage is written again
+                        break;
                 } else {
-                    // eight channels of the warp's rows at a time, through shared memory,
-                    // so that a store instruction writes whole 32-byte sectors
-                    const int r = lane >> 1, q = lane & 1;
-                    float *dst[2];
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bar[PB_MEET4 + quad]);
+                    if (!(ok = wait(PB_MEET4 + quad, met4++ & 1)))
+                        break;
+                    tc_fence_after();          // the other warpgroup's O, which it waited for
+                    const float l0 = l_sum + of->y, l1 = ml[hop].y + of[hop].y, m1 = ml[hop].x;
+                    const float M = fmaxf(m_ref, m1);
+                    const float w0 = l0 != 0.f ? exp2f(m_ref - M) : 0.f, w1 = l1 != 0.f ? exp2f(m1 - M) : 0.f;
+                    ws[0] = x ? w1 : w0;
+                    ws[1] = x ? w0 : w1;
+                    l_sum = (l0 != 0.f ? l0 * w0 : 0.f) + (l1 != 0.f ? l1 * w1 : 0.f);
+                    m_ref = M;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bar[PB_MEET4 + quad]);
+                    if (!(ok = wait(PB_MEET4 + quad, met4++ & 1)))
+                        break;
+                }
+            }
+            const long long at = (long long)flat * p.Hq + h;
+            if (p.direct) {
+                const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
+                ws[0] *= inv;
+                ws[1] *= inv;
+                if (valid_row && half == 0 && (it.pair || x == 0) && p.lse) {
+                    const int bq = (it.pre ? flat / p.Lq : it.b), tq = flat - bq * p.Lq;
+                    p.lse[((long long)bq * p.Hq + h) * p.Lq + tq] =
+                        l_sum != 0.f ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+                }
+            } else if (valid_row && half == 0 && (it.pair || x == 0)) {
+                p.part_ml[it.part * p.rows + at] = make_float2(m_ref, l_sum);
+            }
+            // rows to store: all of the tile's (direct: an empty row is 0), or those with keys
+            const unsigned stored = __ballot_sync(0xffffffffu, valid_row && (p.direct || l_sum != 0.f));
+            if (stored) {
+                // this thread's channels: half of the row, or a quarter where A and B share it
+                const int ch0 = it.pair ? half * (D / 2) : (half * 2 + x) * (D / 4);
+                const int nch = it.pair ? D / 2 : D / 4;
+                // O was written: in pairs with any tile, else by the streams that had one
+                const bool o0 = it.pair ? first < it.nt : it.nt > 0, o1 = !it.pair && it.nt > 1;
+                const uint32_t src = it.pair ? tl + TM_O + x * 128 : tOA;
+                const int eb = p.direct ? 2 : 4;       // bytes of an element
+                uint8_t *orow = (p.direct ? reinterpret_cast<uint8_t *>(p.o)
+                                          : reinterpret_cast<uint8_t *>(p.part_o + it.part * p.rows * D)) +
+                                (at * D + ch0) * eb;
+                const bool few = __popc(stored) <= 8;
+                // through shared memory, 32 bytes of a row at a time, so that a store
+                // instruction writes whole sectors of sixteen rows
+                const int r = lane >> 1, q = lane & 1;
+                uint8_t *dst[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    dst[k] = reinterpret_cast<uint8_t *>(__shfl_sync(
+                                 0xffffffffu, reinterpret_cast<unsigned long long>(orow), r + 16 * k)) + 16 * q;
+                const uint8_t *get = stage + r * 32 + ((q ^ ((r >> 2) & 1)) << 4);
+                uint8_t *put = stage + lane * 32, *put1;
+                put1 = put + ((((lane >> 2) & 1) ^ 1) << 4);
+                put += ((lane >> 2) & 1) << 4;
+                auto put32 = [&](int off, const uint4 &lo, const uint4 &hi) {
+                    if (few) {                 // each lane writes its own row
+                        if ((stored >> lane) & 1) {
+                            *reinterpret_cast<uint4 *>(orow + off) = lo;
+                            *reinterpret_cast<uint4 *>(orow + off + 16) = hi;
+                        }
+                        return;
+                    }
+                    *reinterpret_cast<uint4 *>(put) = lo;
+                    *reinterpret_cast<uint4 *>(put1) = hi;
+                    __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        dst[k] = reinterpret_cast<float *>(__shfl_sync(
-                                     0xffffffffu, reinterpret_cast<unsigned long long>(orow), r + 16 * k)) + 4 * q;
-                    const uint8_t *src = stage + r * 32 + ((q ^ ((r >> 2) & 1)) << 4);
-                    uint8_t *put = stage + lane * 32 + (((lane >> 2) & 1) << 4);
+                        if ((stored >> (r + 16 * k)) & 1)
+                            *reinterpret_cast<uint4 *>(dst[k] + off) = *reinterpret_cast<const uint4 *>(get + k * 512);
+                    __syncwarp();
+                };
 #pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 32) {
-                        float ov[32];
-                        tmem_ld32(tO + c, ov);
+                for (int c = 0; c < nch; c += 16) {
+                    float ov[16];
+                    if (o0) {
+                        tmem_ld16(src + ch0 + c, ov);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            ov[e] = 0.f;
+                    }
+                    if (o1) {
+                        float o2[16];
+                        tmem_ld16(src + 128 + ch0 + c, o2);
+                        tmem_ld_wait();
+                        // (a stream without keys for this row left nothing that counts)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            ov[e] = (ws[0] != 0.f ? ov[e] * ws[0] : 0.f) + (ws[1] != 0.f ? o2[e] * ws[1] : 0.f);
+                    } else {
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            *reinterpret_cast<float4 *>(put) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
-                            *reinterpret_cast<float4 *>(stage + ((put - stage) ^ 16)) =
-                                make_float4(ov[e + 4], ov[e + 5], ov[e + 6], ov[e + 7]);
-                            __syncwarp();
+                        for (int e = 0; e < 16; ++e)
+                            ov[e] = ws[0] != 0.f ? ov[e] * ws[0] : 0.f;
+                    }
+                    if (p.direct) {
+                        uint32_t pk[8];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                if ((stored >> (r + 16 * k)) & 1)
-                                    *reinterpret_cast<float4 *>(dst[k] + c + e) =
-                                        *reinterpret_cast<const float4 *>(src + k * 512);
-                            __syncwarp();
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            pk[e] = pack_bf16x2(ov[2 * e], ov[2 * e + 1]);
+                        put32(c * 2, make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8)
+                            put32((c + e) * 4,
+                                  make_uint4(__float_as_uint(ov[e]), __float_as_uint(ov[e + 1]),
+                                             __float_as_uint(ov[e + 2]), __float_as_uint(ov[e + 3])),
+                                  make_uint4(__float_as_uint(ov[e + 4]), __float_as_uint(ov[e + 5]),
+                                             __float_as_uint(ov[e + 6]), __float_as_uint(ov[e + 7])));
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && first < it.nt)
-                mbar_arrive(&bar[PB_OE + x]);
+            if (lane == 0) {
+                if (it.pair) {
+                    if (first < it.nt) {
+                        mbar_arrive(&bar[PB_OE + x]);
+                        mbar_arrive(&bar[PB_OE + x]);
+                    }
+                } else {
+                    if (it.nt > 0)
+                        mbar_arrive(&bar[PB_OE + 0]);
+                    if (it.nt > 1)
+                        mbar_arrive(&bar[PB_OE + 1]);
+                }
+            }
             theirs += turns ? it.nt : it.pair ? (x ? it.nt : 0) : (it.nt + x) / 2;
             ++nq;
         }
@@ -861,7 +970,6 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams 
             const int tile = ((int)t / p.tpt) * p.nht + ht;
             const int i = ((int)b * p.Hkv + kvh) * p.o_units + (p.o_pair ? tile >> 1 : tile);
             no = pf_cta(p, (i + 1) * p.o_len - 1) - pf_cta(p, i * p.o_len) + 1;
-            no *= p.o_pair ? 1 : 2;
         }
     }
     float M = -INFINITY, L = 0.f;
@@ -933,8 +1041,12 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams 
         p.lse[(b * p.Hq + h) * p.Lq + t] = L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// How the work is split: fills the tiling and the split of p.  False when the
-// own-key stream does not fit 32-bit arithmetic.
+// How the work is split: fills the tiling and the split of p, by the costs below
+// (1/8 us, measured on one B200 at d = 128).  False when the own-key stream does
+// not fit 32-bit arithmetic.
+constexpr int kPfPairCost = 17, kPfAltCost = 8, kPfItemCost = 20;   // a key tile of each mode; an item beside its tiles
+constexpr int kPfJoinCost = 24;                                     // the second kernel
+
 static bool prefix_plan(PrefixParams &p, int d)
 {
     auto up = [](long long a, long long b) { return (a + b - 1) / b; };
@@ -949,102 +1061,117 @@ static bool prefix_plan(PrefixParams &p, int d)
     p.p_units = p.p_pair ? (p.p_tiles + 1) / 2 : 1;
     p.o_units = p.o_pair ? (p.o_tiles + 1) / 2 : 1;
     p.rows = (long long)p.B * p.Lq * p.Hq;
+    p.ctas = kPfPlanSMs;
     // key tiles of the two streams (raw rows: those of consecutive positions)
     const long long span = p.Lq < 2 * p.tpt ? p.Lq : 2 * p.tpt;
     long long raw = p.W > 0 ? (long long)p.W + span - 1 : 0;
     if (raw > p.Lkv)
         raw = p.Lkv;
-    const long long Tp = up(p.Np, kPfBN);
-    long long To = up(p.Nc, kPfBN) + up(raw, kPfBN);
-    const long long Ip = Tp ? (long long)p.p_units * p.Hkv : 0;
-    const long long Io = p.Nc > 0 || p.W > 0 ? (long long)p.o_units * p.Hkv * p.B : 0;
-    if (To < 1)
-        To = 1;
-    // Costs in units of 1/8 us, measured: a key tile of a pair, one of an
-    // alternating item, what an item costs beside its tiles.
-    const long long wp = p.p_pair ? kPfPairCost : kPfAltCost, wo = p.o_pair ? kPfPairCost : kPfAltCost, over = kPfItemCost;
+    const long long Tp = up(p.Np, kPfBN), To = up(p.Nc, kPfBN) + up(raw, kPfBN);
+    const bool own = p.Nc > 0 || p.W > 0;
+    const long long items = (long long)p.o_units * p.Hkv * p.B;       // of own keys
+    const long long wp = p.p_pair ? kPfPairCost : kPfAltCost, wo = p.o_pair ? kPfPairCost : kPfAltCost;
+    const long long over = kPfItemCost, least = over + wo;            // a share worth its overhead
     p.o_over = (int)over;
-    const long long olen = To * wo + over, total_o = Io * olen;
-    if (total_o >= (1LL << 30))
-        return false;
-    p.o_len = (int)olen;
-    // Pieces of the shared entries: the number for which the longest CTA, plus the
-    // traffic of the parts (written and read once, about 4 TB/s), is shortest.
-    // Own keys fill up the CTAs with fewer pieces, or all of them evenly: shares a
-    // (CTAs with one piece more) and b; a share that cuts an item pays `over` again.
-    const double part = (double)p.rows * (d * 4 + 8) * 2 / 4e6 * 8 * (p.p_pair ? 1 : 2);
-    const long long least = over + wo;            // a share worth its overhead
+    // the traffic of one part of every row, written and read once at about 4 TB/s
+    const double part = (double)p.rows * (d * 4 + 8) * 2 / 4e6 * 8;
     double best = -1;
-    long long a = 0, b = least, cnt = 0, rem = 0;
-    p.ctas = kPfPlanSMs;
-    for (long long len = Ip ? Tp : 1, ns_last = 0; len >= 1; len -= 1 + len / 8) {
-        const long long ns = Ip ? up(Tp, len) : 0;
-        if (ns > kPfPlanSMs)
-            break;
-        if (Ip && ns == ns_last)
-            continue;
-        ns_last = ns;
-        const long long piece = Ip ? up(Tp, ns) * wp + over : 0, pieces = Ip * ns;
-        const long long n = pieces / p.ctas, r = pieces % p.ctas;
-        const long long quota = up(pieces * piece + total_o, p.ctas);
-        for (int even = 0; even < 2; ++even) {
-            long long sa = quota - (n + 1) * piece, sb = quota - n * piece;
-            if (r == 0)
-                sa = sb;
-            if (even || sa < least) {
-                sa = 0;
-                sb = up(total_o, p.ctas - r);
-            }
-            if (sb < least)
-                sb = least;
-            const long long cut = total_o && sb < 8 * olen ? over : 0;
-            long long longest = n * piece + (total_o ? sb : 0) + cut;
-            const long long other = (r ? (n + 1) * piece + sa + (sa ? cut : 0) : 0);
-            if (other > longest)
-                longest = other;
-            const double cost = (double)longest + part * ns;
-            if (best < 0 || cost < best) {
-                best = cost;
-                p.p_ns = (int)ns;
-                cnt = n;
-                rem = r;
-                a = sa;
-                b = sb;
-            }
-            if (!total_o)
-                break;
+    long long a = 0, b = least, rem = 0, ns = 0, olen = 1, total = 0;
+    bool merged = false, direct = false;
+    auto take = [&](double cost, bool mg, bool di, long long ns_, long long rem_, long long a_, long long b_,
+                    long long olen_, long long total_) {
+        if (best >= 0 && cost >= best)
+            return;
+        best = cost;
+        merged = mg;
+        direct = di;
+        ns = ns_;
+        rem = rem_;
+        a = a_;
+        b = b_;
+        olen = olen_;
+        total = total_;
+    };
+    // one stream a sequence, through the shared entries as well: whole items, or cut
+    if (Tp + To > 0) {
+        const long long len = (Tp + To) * wo + over, all = items * len;
+        const long long each = up(items, p.ctas);
+        if (all < (1LL << 30)) {
+            take((double)each * len, true, true, 0, 0, each * len, each * len, len, all);
+            long long share = up(all, p.ctas);
+            if (share < least)
+                share = least;
+            if (share < len)
+                take((double)(share + over) + part * (double)(len / share + 1) + kPfJoinCost, true, false, 0, 0, share,
+                     share, len, all);
         }
-        if (!Ip)
-            break;
     }
-    (void)cnt;
-    p.p_pieces = (int)(Ip * p.p_ns);
-    p.p_parts = p.p_ns * (p.p_pair ? 1 : 2);
-    if (b >= 8 * olen) {     // many items a CTA: whole ones, so that no row has a second part
-        a = up(a, olen) * olen;
-        b = up(b, olen) * olen;
+    // Shared entries apart, as ns pieces of each of their items; own keys fill up the
+    // CTAs with fewer pieces, or the others evenly: shares a (CTAs with one piece
+    // more) and b; a share that cuts an item pays `over` again.
+    if (Tp > 0) {
+        const long long len = To * wo + over, all = own ? items * len : 0, Ip = (long long)p.p_units * p.Hkv;
+        for (long long tiles = Tp, last = 0; tiles >= 1 && all < (1LL << 30); tiles -= 1 + tiles / 8) {
+            const long long n = up(Tp, tiles);
+            if (n > p.ctas)
+                break;
+            if (n == last)
+                continue;
+            last = n;
+            const long long piece = up(Tp, n) * wp + over, pieces = Ip * n;
+            const long long cnt = pieces / p.ctas, r = pieces % p.ctas;
+            const long long quota = up(pieces * piece + all, p.ctas);
+            for (int even = 0; even < (all ? 2 : 1); ++even) {
+                long long sa = quota - (cnt + 1) * piece, sb = quota - cnt * piece;
+                if (r == 0)
+                    sa = sb;
+                if (even || sa < least) {
+                    sa = 0;
+                    sb = up(all, p.ctas - r);
+                }
+                if (sb < least)
+                    sb = least;
+                if (sb >= 8 * len) {     // many items a CTA: whole ones, so that no row has a second part
+                    sa = up(sa, len) * len;
+                    sb = up(sb, len) * len;
+                }
+                const bool cut = all && sb % len != 0;
+                long long longest = cnt * piece + (all ? sb : 0) + (cut ? over : 0);
+                const long long other = r ? (cnt + 1) * piece + sa + (sa && cut ? over : 0) : 0;
+                if (other > longest)
+                    longest = other;
+                take((double)longest + part * (double)(n + (all ? 1 + cut : 0)) + kPfJoinCost, false, false, n, r, sa,
+                     sb, len, all);
+            }
+        }
     }
-    p.o_rem = a > 0 || rem < p.ctas ? (int)rem : 0;
+    if (Tp + To > 0 && best < 0)
+        return false;
+    p.merged = merged;
+    p.direct = direct;
+    p.p_ns = (int)ns;
+    p.p_parts = (int)ns;
+    p.p_pieces = (int)(ns * p.p_units * p.Hkv);
+    p.o_len = (int)olen;
+    p.o_rem = (int)rem;
     p.o_a = (int)a;
     p.o_b = (int)b;
-    p.o_total = Io ? (int)total_o : 0;
+    p.o_total = (int)total;
     // most CTAs that an own item can be spread over
     long long o_parts = 0;
-    if (Io) {
+    if (total > 0 && !direct) {
         const long long small = a > 0 && a < b ? a : b;
         o_parts = b % olen == 0 && a % olen == 0 ? 1 : (olen - 2) / small + 2;
-        if (total_o <= small)
+        if (total <= small)
             o_parts = 1;
         if (o_parts > p.ctas)
             o_parts = p.ctas;
-        o_parts *= p.o_pair ? 1 : 2;
     }
     p.n_parts = p.p_parts + (int)o_parts;
     // CTAs with something to do
-    int last = p.p_pieces < p.ctas ? p.p_pieces : p.ctas;
-    if (Io && pf_cta(p, p.o_total - 1) + 1 > last)
-        last = pf_cta(p, p.o_total - 1) + 1;
-    p.ctas_used = last;
+    p.ctas_used = p.p_pieces < p.ctas ? p.p_pieces : p.ctas;
+    if (total > 0 && pf_cta(p, p.o_total - 1) + 1 > p.ctas_used)
+        p.ctas_used = pf_cta(p, p.o_total - 1) + 1;
     return true;
 }
 
@@ -1079,7 +1206,7 @@ static cudaError_t launch_prefix_t(PrefixParams &p, const void *q, const void *k
         // absent tensors: a map that no copy uses
         CUtensorMap mqp, mqo, mkp, mvp, mkc, mvc, mkr, mvr;
         bool ok = make_map(&mqp, q, D, p.Hq, p.B * p.Lq, 1, p.hpt, p.tpt);
-        if (p.p_pieces > 0) {
+        if (p.Np > 0) {
             ok &= make_map(&mkp, kp, D, p.Hkv, p.Np, 1, 1, kPfBN);
             ok &= make_map(&mvp, vp, D, p.Hkv, p.Np, 1, 1, kPfBN);
         } else {
@@ -1125,6 +1252,8 @@ static cudaError_t launch_prefix_t(PrefixParams &p, const void *q, const void *k
         if (e != cudaSuccess)
             return e;
     }
+    if (p.direct)
+        return cudaSuccess;
     // with eight parts a lane group or more, eight groups share a row
     constexpr int GROUPS = 256 / (D / 4);
     if (p.n_parts >= 64)
