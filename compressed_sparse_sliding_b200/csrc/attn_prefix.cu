@@ -18,8 +18,9 @@
 //              tiles are fetched once for 256 rows);
 //   alternate  where there is a single query tile, the two softmax warpgroups
 //              take its even and odd key tiles, each with its own maximum, sum
-//              and O (HBM-bound: twice the tiles in flight), and join them in
-//              TMEM: every warp can read both O's of its lanes.
+//              and O (HBM-bound: twice the tiles in flight), and store two parts
+//              (or join them in TMEM, where every warp can read both O's of its
+//              lanes, if nothing else follows).
 // Where a sequence's own query rows fill the tiles (chunks of a prompt), or the
 // prefix is short, the shared entries are not taken apart: an item's stream then is
 // prefix, own entries, window, and if no item is cut the kernel writes o itself, with
@@ -229,9 +230,8 @@ __device__ __forceinline__ int pf_visible(long long pos, int m, int W, int n)
     const long long a = pos - W + 1;
     if (a <= 0)
         return 0;
-    const unsigned long long v = (unsigned long long)a < (1ull << 32) ? (unsigned)a / (unsigned)m
-                                                                       : (unsigned long long)a / (unsigned)m;
-    return v < (unsigned long long)n ? (int)v : n;
+    const unsigned v = (unsigned)a / (unsigned)m;     // positions are 32-bit
+    return v < (unsigned)n ? (int)v : n;
 }
 
 // First unit of CTA k's share of the own-key stream, and the CTA a unit is in.
@@ -248,10 +248,23 @@ __host__ __device__ __forceinline__ int pf_cta(const PrefixParams &p, int u)
     return u < head ? u / p.o_a : p.o_rem + (u - head) / p.o_b;
 }
 
+// a * b / c of non-negative numbers (a 64-bit division is a hundred instructions,
+// which the items of short streams would fetch again and again).
+__device__ __noinline__ int pf_muldiv64(int a, int b, int c)
+{
+    return (int)((long long)a * b / c);
+}
+
+__device__ __forceinline__ int pf_muldiv(int a, int b, int c)
+{
+    return __umulhi((unsigned)a, (unsigned)b) == 0 ? (int)((unsigned)a * (unsigned)b / (unsigned)c)
+                                                   : pf_muldiv64(a, b, c);
+}
+
 // Key tiles before unit u of an item of T tiles.
 __device__ __forceinline__ int pf_cut(const PrefixParams &p, int T, int u)
 {
-    return (int)((long long)T * max(u - p.o_over, 0) / (p.o_len - p.o_over));
+    return pf_muldiv(T, max(u - p.o_over, 0), p.o_len - p.o_over);
 }
 
 // Works out one item (whole warp): piece `s` of p_ns of the shared entries for
@@ -268,7 +281,7 @@ __device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int
         u = i % p.p_units;
         it.kvh = i / p.p_units;
         it.b = 0;
-        it.part = s;
+        it.part = it.pair ? s : 2 * s;
         it.ntok = p.B * p.Lq;
     } else {
         it.pair = p.o_pair;
@@ -276,7 +289,7 @@ __device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int
         const int r = i / p.o_units;
         it.kvh = r % p.Hkv;
         it.b = r / p.Hkv;
-        it.part = p.p_parts + s;
+        it.part = p.p_parts + (it.pair ? s : 2 * s);
         it.ntok = p.Lq;
     }
     const long long kv0 = !pre && p.kv_pos0 ? p.kv_pos0[it.b] : 0;
@@ -322,8 +335,8 @@ __device__ __forceinline__ void prefix_item(const PrefixParams &p, bool pre, int
     it.nte = (it.nent + kPfBN - 1) / kPfBN;
     const int T = it.ntp + it.nte + (it.nraw + kPfBN - 1) / kPfBN;
     if (pre) {
-        it.t0 = (int)((long long)T * s / p.p_ns);
-        it.nt = (int)((long long)T * (s + 1) / p.p_ns) - it.t0;
+        it.t0 = pf_muldiv(T, s, p.p_ns);
+        it.nt = pf_muldiv(T, s + 1, p.p_ns) - it.t0;
     } else {
         it.t0 = pf_cut(p, T, u0);
         it.nt = (u1 == p.o_len ? T : pf_cut(p, T, u1)) - it.t0;
@@ -367,7 +380,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             mbar_init(&bar[PB_SF + s], 1);
             mbar_init(&bar[PB_PF + s], 8);     // one arrival a warp
             mbar_init(&bar[PB_OF + s], 1);
-            mbar_init(&bar[PB_OE + s], 16);    // both warpgroups (alternate), or two from one
+            mbar_init(&bar[PB_OE + s], 16);    // both warpgroups (joint), or two from one
         }
         for (int s = 0; s < kPfItemSlots; ++s) {
             mbar_init(&bar[PB_IF + s], 1);
@@ -779,9 +792,82 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 ++ocnt;
                 tc_fence_after();
             }
-            // The row's sum over both halves, and in an alternating item the two
+            if (!p.direct) {
+                // a part of the row: this warpgroup's O as it is, its maximum and sum
+                if (warp_rows) {
+                    *mine = l_sum;
+                    if (!(ok = meet()))
+                        break;
+                    l_sum += *other;
+                    if (!(ok = meet()))      // before the next item's first maximum
+                        break;
+                }
+                const size_t at = (size_t)(it.part + (it.pair ? 0 : x)) * p.rows + (size_t)flat * p.Hq + h;
+                if (valid_row && half == 0)
+                    p.part_ml[at] = make_float2(m_ref, l_sum);
+                const unsigned stored = __ballot_sync(0xffffffffu, valid_row && l_sum != 0.f);
+                if (stored) {
+                    float *orow = p.part_o + at * D + half * (D / 2);
+                    if (__popc(stored) <= 8) {
+                        // few rows: each lane writes its own
+#pragma unroll 1
+                        for (int c = 0; c < D / 2; c += 32) {
+                            float ov[32];
+                            tmem_ld32(tO + c, ov);
+                            tmem_ld_wait();
+                            if ((stored >> lane) & 1) {
+#pragma unroll
+                                for (int q = 0; q < 32; q += 4)
+                                    *reinterpret_cast<float4 *>(orow + c + q) =
+                                        make_float4(ov[q], ov[q + 1], ov[q + 2], ov[q + 3]);
+                            }
+                        }
+                    } else {
+                        // eight channels of the warp's rows at a time, through shared memory,
+                        // so that a store instruction writes whole 32-byte sectors
+                        const int r = lane >> 1, q = lane & 1;
+                        float *dst[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            dst[k] = reinterpret_cast<float *>(__shfl_sync(
+                                         0xffffffffu, reinterpret_cast<unsigned long long>(orow), r + 16 * k)) + 4 * q;
+                        const uint8_t *src = stage + r * 32 + ((q ^ ((r >> 2) & 1)) << 4);
+                        uint8_t *put = stage + lane * 32 + (((lane >> 2) & 1) << 4);
+#pragma unroll 1
+                        for (int c = 0; c < D / 2; c += 32) {
+                            float ov[32];
+                            tmem_ld32(tO + c, ov);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                *reinterpret_cast<float4 *>(put) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                                *reinterpret_cast<float4 *>(stage + ((put - stage) ^ 16)) =
+                                    make_float4(ov[e + 4], ov[e + 5], ov[e + 6], ov[e + 7]);
+                                __syncwarp();
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    if ((stored >> (r + 16 * k)) & 1)
+                                        *reinterpret_cast<float4 *>(dst[k] + c + e) =
+                                            *reinterpret_cast<const float4 *>(src + k * 512);
+                                __syncwarp();
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && first < it.nt) {
+                    mbar_arrive(&bar[PB_OE + x]);
+                    mbar_arrive(&bar[PB_OE + x]);
+                }
+                theirs += turns ? it.nt : it.pair ? (x ? it.nt : 0) : (it.nt + x) / 2;
+                ++nq;
+                continue;
+            }
+            // The row's sum over both halves, and where an alternating item is joined the two
             // streams' maxima and sums: weights ws of this warpgroup's (pair) or of A's
             // and B's O, maximum m_ref and sum l_sum of the result.
+            const bool joint = !it.pair;
             float ws[2] = {1.f, 0.f};
             if (warp_rows) {
                 float2 *ml = reinterpret_cast<float2 *>(stage) + lane;
@@ -789,7 +875,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 const int hop = ((warp ^ 8) - warp) * SM::STAGE_BYTES / (int)sizeof(float2);
                 *ml = make_float2(m_ref, l_sum);
                 tc_fence_before();
-                if (it.pair) {
+                if (!joint) {
                     if (!(ok = meet()))
                         break;
                     l_sum += of->y;
@@ -817,31 +903,21 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 }
             }
             const long long at = (long long)flat * p.Hq + h;
-            if (p.direct) {
-                const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
-                ws[0] *= inv;
-                ws[1] *= inv;
-                if (valid_row && half == 0 && (it.pair || x == 0) && p.lse) {
-                    const int bq = (it.pre ? flat / p.Lq : it.b), tq = flat - bq * p.Lq;
-                    p.lse[((long long)bq * p.Hq + h) * p.Lq + tq] =
-                        l_sum != 0.f ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
-                }
-            } else if (valid_row && half == 0 && (it.pair || x == 0)) {
-                p.part_ml[it.part * p.rows + at] = make_float2(m_ref, l_sum);
-            }
-            // rows to store: all of the tile's (direct: an empty row is 0), or those with keys
-            const unsigned stored = __ballot_sync(0xffffffffu, valid_row && (p.direct || l_sum != 0.f));
+            const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
+            ws[0] *= inv;
+            ws[1] *= inv;
+            if (valid_row && half == 0 && (!joint || x == 0) && p.lse)
+                p.lse[((long long)it.b * p.Hq + h) * p.Lq + flat - it.b * p.Lq] =
+                    l_sum != 0.f ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+            const unsigned stored = __ballot_sync(0xffffffffu, valid_row);    // (an empty row is 0)
             if (stored) {
                 // this thread's channels: half of the row, or a quarter where A and B share it
-                const int ch0 = it.pair ? half * (D / 2) : (half * 2 + x) * (D / 4);
-                const int nch = it.pair ? D / 2 : D / 4;
+                const int ch0 = joint ? (half * 2 + x) * (D / 4) : half * (D / 2);
+                const int nch = joint ? D / 4 : D / 2;
                 // O was written: in pairs with any tile, else by the streams that had one
-                const bool o0 = it.pair ? first < it.nt : it.nt > 0, o1 = !it.pair && it.nt > 1;
-                const uint32_t src = it.pair ? tl + TM_O + x * 128 : tOA;
-                const int eb = p.direct ? 2 : 4;       // bytes of an element
-                uint8_t *orow = (p.direct ? reinterpret_cast<uint8_t *>(p.o)
-                                          : reinterpret_cast<uint8_t *>(p.part_o + it.part * p.rows * D)) +
-                                (at * D + ch0) * eb;
+                const bool o0 = joint ? it.nt > 0 : first < it.nt, o1 = joint && it.nt > 1;
+                const uint32_t src = joint ? tOA : tl + TM_O + x * 128;
+                uint8_t *orow = reinterpret_cast<uint8_t *>(p.o + at * D + ch0);
                 const bool few = __popc(stored) <= 8;
                 // through shared memory, 32 bytes of a row at a time, so that a store
                 // instruction writes whole sectors of sixteen rows
@@ -896,27 +972,17 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                         for (int e = 0; e < 16; ++e)
                             ov[e] = ws[0] != 0.f ? ov[e] * ws[0] : 0.f;
                     }
-                    if (p.direct) {
-                        uint32_t pk[8];
+                    uint32_t pk[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            pk[e] = pack_bf16x2(ov[2 * e], ov[2 * e + 1]);
-                        put32(c * 2, make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 8)
-                            put32((c + e) * 4,
-                                  make_uint4(__float_as_uint(ov[e]), __float_as_uint(ov[e + 1]),
-                                             __float_as_uint(ov[e + 2]), __float_as_uint(ov[e + 3])),
-                                  make_uint4(__float_as_uint(ov[e + 4]), __float_as_uint(ov[e + 5]),
-                                             __float_as_uint(ov[e + 6]), __float_as_uint(ov[e + 7])));
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        pk[e] = pack_bf16x2(ov[2 * e], ov[2 * e + 1]);
+                    put32(c * 2, make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]));
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (it.pair) {
+                if (!joint) {
                     if (first < it.nt) {
                         mbar_arrive(&bar[PB_OE + x]);
                         mbar_arrive(&bar[PB_OE + x]);
@@ -970,6 +1036,7 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams 
             const int tile = ((int)t / p.tpt) * p.nht + ht;
             const int i = ((int)b * p.Hkv + kvh) * p.o_units + (p.o_pair ? tile >> 1 : tile);
             no = pf_cta(p, (i + 1) * p.o_len - 1) - pf_cta(p, i * p.o_len) + 1;
+            no *= p.o_pair ? 1 : 2;
         }
     }
     float M = -INFINITY, L = 0.f;
@@ -1044,7 +1111,8 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const PrefixParams 
 // How the work is split: fills the tiling and the split of p, by the costs below
 // (1/8 us, measured on one B200 at d = 128).  False when the own-key stream does
 // not fit 32-bit arithmetic.
-constexpr int kPfPairCost = 17, kPfAltCost = 8, kPfItemCost = 20;   // a key tile of each mode; an item beside its tiles
+constexpr int kPfPairCost = 17, kPfAltCost = 8;           // a key tile of each mode
+constexpr int kPfPairItemCost = 40, kPfAltItemCost = 20;  // an item beside its tiles (256 or a few rows to store)
 constexpr int kPfJoinCost = 24;                                     // the second kernel
 
 static bool prefix_plan(PrefixParams &p, int d)
@@ -1071,7 +1139,8 @@ static bool prefix_plan(PrefixParams &p, int d)
     const bool own = p.Nc > 0 || p.W > 0;
     const long long items = (long long)p.o_units * p.Hkv * p.B;       // of own keys
     const long long wp = p.p_pair ? kPfPairCost : kPfAltCost, wo = p.o_pair ? kPfPairCost : kPfAltCost;
-    const long long over = kPfItemCost, least = over + wo;            // a share worth its overhead
+    const long long over_p = p.p_pair ? kPfPairItemCost : kPfAltItemCost;
+    const long long over = p.o_pair ? kPfPairItemCost : kPfAltItemCost, least = over + wo;   // a share worth its overhead
     p.o_over = (int)over;
     // the traffic of one part of every row, written and read once at about 4 TB/s
     const double part = (double)p.rows * (d * 4 + 8) * 2 / 4e6 * 8;
@@ -1102,7 +1171,7 @@ static bool prefix_plan(PrefixParams &p, int d)
             if (share < least)
                 share = least;
             if (share < len)
-                take((double)(share + over) + part * (double)(len / share + 1) + kPfJoinCost, true, false, 0, 0, share,
+                take((double)(share + over) + part * (double)((len / share + 1) * (p.o_pair ? 1 : 2)) + kPfJoinCost, true, false, 0, 0, share,
                      share, len, all);
         }
     }
@@ -1118,7 +1187,7 @@ static bool prefix_plan(PrefixParams &p, int d)
             if (n == last)
                 continue;
             last = n;
-            const long long piece = up(Tp, n) * wp + over, pieces = Ip * n;
+            const long long piece = up(Tp, n) * wp + over_p, pieces = Ip * n;
             const long long cnt = pieces / p.ctas, r = pieces % p.ctas;
             const long long quota = up(pieces * piece + all, p.ctas);
             for (int even = 0; even < (all ? 2 : 1); ++even) {
@@ -1140,7 +1209,7 @@ static bool prefix_plan(PrefixParams &p, int d)
                 const long long other = r ? (cnt + 1) * piece + sa + (sa && cut ? over : 0) : 0;
                 if (other > longest)
                     longest = other;
-                take((double)longest + part * (double)(n + (all ? 1 + cut : 0)) + kPfJoinCost, false, false, n, r, sa,
+                take((double)longest + part * (double)(n * (p.p_pair ? 1 : 2) + (all ? (1 + cut) * (p.o_pair ? 1 : 2) : 0)) + kPfJoinCost, false, false, n, r, sa,
                      sb, len, all);
             }
         }
@@ -1150,7 +1219,7 @@ static bool prefix_plan(PrefixParams &p, int d)
     p.merged = merged;
     p.direct = direct;
     p.p_ns = (int)ns;
-    p.p_parts = (int)ns;
+    p.p_parts = (int)ns * (p.p_pair ? 1 : 2);
     p.p_pieces = (int)(ns * p.p_units * p.Hkv);
     p.o_len = (int)olen;
     p.o_rem = (int)rem;
@@ -1166,6 +1235,7 @@ static bool prefix_plan(PrefixParams &p, int d)
             o_parts = 1;
         if (o_parts > p.ctas)
             o_parts = p.ctas;
+        o_parts *= p.o_pair ? 1 : 2;
     }
     p.n_parts = p.p_parts + (int)o_parts;
     // CTAs with something to do

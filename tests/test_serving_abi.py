@@ -33,11 +33,18 @@ def _prefix(hb, Np=8, ws_bytes=1 << 30, swap=None, **kw):
     (dict(Lq=0), "INVALID_ARG"), (dict(m=0), "INVALID_ARG"), (dict(W=-1), "INVALID_ARG"),
     (dict(Nc=-1), "INVALID_ARG"), (dict(d=96), "UNSUPPORTED"), (dict(topk=4), "UNSUPPORTED"),
     (dict(Np=1 << 29, Nc=1 << 29), "UNSUPPORTED"), (dict(B=1 << 20, Lq=1 << 12), "UNSUPPORTED"),
-    (dict(W=1 << 30), "UNSUPPORTED"), (dict(ws_bytes=16), "WORKSPACE"), (dict(swap=("ws", None)), "WORKSPACE"),
-    (dict(swap=("ws", 4096 + 16)), "WORKSPACE"),
+    (dict(W=1 << 30), "UNSUPPORTED"), (dict(B=1 << 20, Nc=1 << 16), "UNSUPPORTED"),
 ])
 def test_prefix_refusals(hb, change, status):
     assert _prefix(hb, **change) == getattr(hb, "HYB_ERR_" + status)
+
+
+def test_prefix_refuses_a_missing_short_or_misaligned_workspace(hb):
+    big = dict(B=2, Lq=1, Lkv=16, Hq=4, Hkv=2, d=64, m=4, W=8, Nc=4)
+    need = hb.hyb_prefix_workspace_size(hb.problem(**big), 100000)
+    assert need > 0
+    for bad in (dict(ws_bytes=need - 1), dict(swap=("ws", None)), dict(swap=("ws", 4096 + 16))):
+        assert _prefix(hb, Np=100000, **bad) == hb.HYB_ERR_WORKSPACE
 
 
 @pytest.mark.parametrize("name", ["q", "kp", "vp", "kc", "vc", "k_raw", "v_raw", "o"])
@@ -47,10 +54,12 @@ def test_prefix_refuses_missing_and_misaligned_tensors(hb, name):
 
 
 def test_prefix_workspace(hb):
-    # partial results of every row: (maximum, sum) pairs and fp32 rows of d
+    # partial results of every row: (maximum, sum) pairs and fp32 rows of d; none
+    # where the sequences' streams are short enough to stay whole
     p = hb.problem(B=2, Lq=1, Lkv=16, Hq=4, Hkv=2, d=64, m=4, W=8, Nc=4)
     one = 2 * 4 * (8 + 64 * 4)
-    assert hb.hyb_prefix_workspace_size(p, 8) >= one and hb.hyb_prefix_workspace_size(p, 8) % 256 == 0
+    size = hb.hyb_prefix_workspace_size(p, 100000)
+    assert size >= 2 * one and size % 256 == 0 and hb.hyb_prefix_workspace_size(p, 8) == 0
     # nothing to attend to: nothing to keep
     p = hb.problem(B=2, Lq=1, Lkv=0, Hq=4, Hkv=2, d=64, m=4, W=0, Nc=0)
     assert hb.hyb_prefix_workspace_size(p, 0) == 0
