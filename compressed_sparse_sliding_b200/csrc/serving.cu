@@ -7,6 +7,11 @@
 
 namespace hyb {
 
+static bool aligned4(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
 static bool ws_ok(const void *ws, size_t ws_bytes, size_t need)
 {
     return need == 0 || (ws && ws_bytes >= need && !(reinterpret_cast<uintptr_t>(ws) & 255u));
@@ -46,7 +51,7 @@ static hyb_status check_prefix(const hyb_problem *p, int Np, PrefixParams &a)
 static hyb_status compact_common(const hyb_problem *p, const int32_t *keep, int n_keep, int No,
                                  const CompactTensor *t, int n, cudaStream_t stream)
 {
-    if (!p || p->B <= 0 || p->Nc <= 0 || n_keep <= 0 || No < n_keep || !keep)
+    if (!p || p->B <= 0 || p->Nc <= 0 || n_keep <= 0 || No < n_keep || !keep || !aligned4(keep))
         return HYB_ERR_INVALID_ARG;
     if (p->Nc >= (1 << 30) || No >= (1 << 30))
         return HYB_ERR_UNSUPPORTED;
@@ -102,7 +107,7 @@ hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, cons
     const hyb_status st = check_prefix(p, Np, a);
     if (st != HYB_OK)
         return st;
-    if (!q || !o || !aligned16(q) || !aligned16(o))
+    if (!q || !o || !aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(p->q_pos) || !aligned4(p->kv_pos0))
         return HYB_ERR_INVALID_ARG;
     if (Np > 0 && (!kp || !vp || !aligned16(kp) || !aligned16(vp)))
         return HYB_ERR_INVALID_ARG;
@@ -124,7 +129,8 @@ hyb_status hyb_attn_weights(const hyb_problem *p, const void *q, const void *kc,
     hyb_status st = check_problem(p, false);
     if (st != HYB_OK)
         return st;
-    if (e0 < 0 || !(p->scale >= 0.f) || p->Nc <= 0 || !q || !kc || !lse || !acc || !aligned16(q) || !aligned16(kc))
+    if (e0 < 0 || !(p->scale >= 0.f) || p->Nc <= 0 || !q || !kc || !lse || !acc || !aligned16(q) || !aligned16(kc) ||
+        !aligned4(lse) || !aligned4(acc) || !aligned4(idx) || !aligned4(p->q_pos))
         return HYB_ERR_INVALID_ARG;
     if (!idx != (p->topk <= 0))
         return HYB_ERR_INVALID_ARG;
@@ -143,7 +149,7 @@ hyb_status hyb_evict_select(const float *acc, int B, int Nc, const int32_t *n_va
 {
     NvtxRange nvtx_range("hyb_evict_select");
     if (!acc || !keep || B <= 0 || Nc <= 0 || n_keep <= 0 || n_first < 0 || n_last < 0 ||
-        (long long)n_first + n_last > n_keep)
+        (long long)n_first + n_last > n_keep || !aligned4(acc) || !aligned4(n_valid) || !aligned4(keep))
         return HYB_ERR_INVALID_ARG;
     if (B > 65535 || Nc >= (1 << 30) || n_keep >= (1 << 30))
         return HYB_ERR_UNSUPPORTED;

@@ -39,6 +39,14 @@ def test_prefix_refusals(hb, change, status):
     assert _prefix(hb, **change) == getattr(hb, "HYB_ERR_" + status)
 
 
+def test_prefix_refuses_misaligned_fp32_and_int32(hb):
+    assert _prefix(hb, swap=("lse", 4096 + 2)) == hb.HYB_ERR_INVALID_ARG
+    p = hb.problem(B=2, Lq=1, Lkv=16, Hq=4, Hkv=2, d=64, m=4, W=8, Nc=4)
+    p.q_pos = 4096 + 2
+    a = [ctypes.c_void_p(4096)] * 10
+    assert hb._lib.hyb_prefix_attn_fwd(ctypes.byref(p), 8, *a, 1 << 30, None) == hb.HYB_ERR_INVALID_ARG
+
+
 def test_prefix_refuses_a_missing_short_or_misaligned_workspace(hb):
     big = dict(B=2, Lq=1, Lkv=16, Hq=4, Hkv=2, d=64, m=4, W=8, Nc=4)
     need = hb.hyb_prefix_workspace_size(hb.problem(**big), 100000)
@@ -102,6 +110,8 @@ def _weights(hb, e0=0, swap=None, idx=False, **kw):
     (dict(swap=("q", None)), "INVALID_ARG"), (dict(swap=("kc", None)), "INVALID_ARG"),
     (dict(swap=("lse", None)), "INVALID_ARG"), (dict(swap=("acc", None)), "INVALID_ARG"),
     (dict(swap=("q", 4096 + 8)), "INVALID_ARG"), (dict(swap=("kc", 4096 + 2)), "INVALID_ARG"),
+    (dict(swap=("lse", 4096 + 2)), "INVALID_ARG"), (dict(swap=("acc", 4096 + 1)), "INVALID_ARG"),
+    (dict(idx=True, swap=("idx", 4096 + 2)), "INVALID_ARG"),
     (dict(idx=True, Lq=2), "UNSUPPORTED"), (dict(idx=True, topk=2049), "UNSUPPORTED"), (dict(d=32), "UNSUPPORTED"),
     (dict(e0=1 << 30), "UNSUPPORTED"), (dict(B=1 << 20, Lq=1 << 12), "UNSUPPORTED"),
 ])
