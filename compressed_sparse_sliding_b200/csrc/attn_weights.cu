@@ -12,16 +12,23 @@
 //
 // Layout.  S^T = K Q^T on tcgen05: keys are the MMA's M, so a TMEM lane is a key
 // and the sum over query rows stays inside one thread.  Four epilogue warpgroups
-// take key tiles in turn where a CTA has many (with two, each tile's chain of
-// barrier, TMEM load and exponentials was what the copies waited for: 57 us where
-// four take 44), and otherwise share every tile: every fourth 32-row column chunk,
-// the sums added through shared memory.  No atomics between CTAs: each entry has
-// one owner, and equal calls give equal bits.  A CTA owns a run of key tiles of one or more
-// sequences, every CTA the same number of tiles that hold visible entries.  Four
+// take key tiles in turn where a CTA has many (64 sequences x 16384 entries, 64
+// heads: 47.5 us; all four on every tile: 62.2, same GPU and before the waits were
+// shortened), and otherwise share every tile: every fourth 32-row column chunk, the
+// sums added through shared memory.  Each entry has one owner, and equal calls give
+// equal bits (only a selection adds with atomics, for entries listed more than once:
+// their copies are equal, so any order gives the same sum).  A CTA owns a run of key tiles of one or
+// more sequences, every CTA the same number of tiles that hold visible entries.  Four
 // K stages and four S buffers (4 x 128 TMEM columns) keep copies, MMAs and
 // exponentials of different tiles running together.  Query blocks (hpt heads x
 // tpt tokens, up to 128 rows) stay in shared memory for the whole run where all
 // of a sequence's fit 64 KB (decode), and stream through the same slots otherwise.
+//
+// Measured (one B200): 64 sequences x 16384 entries (three quarters visible), 64
+// heads over one KV head of 128: 44.5 us, 4.5 TB/s of K; 1024 selected entries of
+// each: 16 us with the copy of acc before it, of which the gather's and the
+// barriers' latencies are most; 32 query tokens x 32 heads over 2 x 8192 entries:
+// 24 us, one tile a CTA, bound by the streamed query blocks' latency.
 //
 // Roles (768 threads): warps 0-15 epilogue (thread = key), warp 16 TMA producer,
 // warp 17 MMA issue, warps 18 and 19 write the query blocks' lse and visible counts

@@ -240,9 +240,11 @@ hyb_status hyb_gated_fwd(const hyb_problem *p, const void *q, const void *kc, co
  * bf16 and 16-byte aligned; o: [B, Lq, Hq, d] bf16; lse: [B, Hq, Lq] fp32
  * (nullable).  Entries that no query of the batch (shared) or of the sequence
  * (own) sees may hold anything, NaN included; so may raw rows outside a
- * sequence's windows (from its lowest to its highest query position).
- * ws: hyb_prefix_workspace_size(p, Np) bytes, 256-byte aligned; calls that may
- * run at the same time need a workspace each. */
+ * sequence's windows (from its lowest to its highest query position).  What some
+ * query of the call sees has to be finite: a NaN or an infinity in its value row
+ * may also reach queries that do not see it (a weight of 0 times NaN).
+ * ws: hyb_prefix_workspace_size(p, Np) bytes, 256-byte aligned (0 bytes: NULL
+ * will do); calls that may run at the same time need a workspace each. */
 size_t hyb_prefix_workspace_size(const hyb_problem *p, int Np);
 hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, const void *kp, const void *vp,
                                const void *kc, const void *vc, const void *k_raw, const void *v_raw, void *o,
