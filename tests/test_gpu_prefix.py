@@ -8,6 +8,13 @@ d 2^-24 of sum |q||k| scale = e, which moves P and lse by that much, twice for P
 2^-23 of |s| <= e more each.  So, with A = sum P |v| and r = (d + 4) 2^-23 e:
   |o - ref|   <= 2^-8 (|ref| + A) (1 + 2^-8) + 2 r A + 2^-20 A
   |lse - ref| <= r + n 2^-24 + 2^-20 (1 + |ref|)     (n terms in the fp32 sum)
+A quarter of the exponentials come from a polynomial that is off by at most 2.8e-6
+< 2^-18 of the value, which the bounds above hold without a term of their own:
+with u = 2^-8 / (1 + 2^-8) (half a bf16 step, relative to the value) o is off by at most
+u (|ref| + A) + u^2 A + 2 * 2^-18 A < 2^-8 (|ref| + A) - 2^-16 |ref| + 2^-17 A + 2^-23 A,
+less than the first term of its bound; and lse moves by less than 2^-18, while r
+counts the d 2^-24 e of a score twice: the half that is over, (d + 4) 2^-24 e, is more
+than 2^-18 from e = 0.94 on (d = 64; 0.49 at d = 128), and e is above 2 in these inputs.
 """
 import numpy as np
 import pytest
