@@ -17,33 +17,41 @@
 // shortened), and otherwise share every tile: every fourth 32-row column chunk, the
 // sums added through shared memory.  Each entry has one owner, and equal calls give
 // equal bits (only a selection adds with atomics, for entries listed more than once:
-// their copies are equal, so any order gives the same sum).  A CTA owns a run of key tiles of one or
-// more sequences, every CTA the same number of tiles that hold visible entries.  Four
-// K stages and four S buffers (4 x 128 TMEM columns) keep copies, MMAs and
-// exponentials of different tiles running together.  Query blocks (hpt heads x
-// tpt tokens, up to 128 rows) stay in shared memory for the whole run where all
-// of a sequence's fit 64 KB (decode), and stream through the same slots otherwise.
+// their copies are equal, so any order gives the same sum).  A CTA owns a run of key
+// tiles of one or more sequences, every CTA the same number of tiles that hold visible
+// entries.  Four S buffers (4 x 128 TMEM columns) and the K stages keep copies, MMAs
+// and exponentials of different tiles running together.  Query blocks (hpt heads x
+// tpt tokens, up to 128 rows) stay in shared memory for the whole run where all of a
+// sequence's fit 64 KB (decode: four K stages).  Otherwise they stream, through twice
+// the bytes and beside two K stages, since a K tile then serves many blocks.
 //
 // Measured (one B200): 64 sequences x 16384 entries (three quarters visible), 64
-// heads over one KV head of 128: 44.5 us, 4.5 TB/s of K; 1024 selected entries of
-// each: 16 us with the copy of acc before it, of which the gather's and the
+// heads over one KV head of 128: 43.4 us, 4.6 TB/s of K; 1024 selected entries of
+// each: 17 us with the copy of acc before it, of which the gather's and the
 // barriers' latencies are most; 32 query tokens x 32 heads over 2 x 8192 entries:
-// 24 us, one tile a CTA, bound by the streamed query blocks' latency.
+// 16.6 us.  A streamed block takes about 1 us of a CTA: what writes its lse and counts
+// was most of it (128 tokens: 54.8 us with two warps for that, 36.5 with the loads
+// left out, 40.2 with four warps), and a tile that some query tokens do not see whole
+// costs more than the others, so that the CTA that has it ends last (scalar reads
+// of lse and counts there: 24.0 us in place of 19).
 //
 // Roles (768 threads): warps 0-15 epilogue (thread = key), warp 16 TMA producer,
-// warp 17 MMA issue, warps 18 and 19 write the query blocks' lse and visible counts
-// beside them (even and odd slots), warps 20-23 gather the selected rows with cp.async when idx is given
-// (16 lanes per row).
+// warp 17 MMA issue, warps 18 and 19 (without a selection 18 to 21) write the query
+// blocks' lse and visible counts beside them, a slot always by the same warp; warps
+// 20-23 gather the selected rows with cp.async when idx is given (16 lanes per row).
 #include "common.cuh"
 
 namespace hyb {
 
 constexpr int kAwThreads = 768;
 constexpr int kAwWgs = 4;           // epilogue warpgroups
+// 512 x 88 + 256 x 64 = 768 x 80 (the launch's registers); one share for all spills
+// more: 46.0 us for the decode case above where the split takes 44.4
+constexpr int kAwEpiRegs = 88, kAwOtherRegs = 64;
 constexpr int kAwBM = 128;          // keys of a tile
-constexpr int kAwKStages = 4;
+constexpr int kAwKStages = 4;       // with resident queries; 2 with streamed ones
 constexpr int kAwSBufs = 4;
-constexpr int kAwQBytes = 64 * 1024;
+constexpr int kAwQBytes = 64 * 1024;   // resident queries; streamed ones have two K stages' bytes more
 constexpr int kAwQStages = 16;      // barrier slots; the bytes usually bind first
 // Sequences whose visible counts a CTA sums up at its start, to cut the stream of
 // all visible tiles evenly, and the positions it reads for that; with more, a
@@ -73,7 +81,9 @@ struct WeightSmem {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = kAwQBytes;
     static constexpr int OFF_COL = OFF_K + kAwKStages * K_BYTES;     // -lse (log2) per column, then counts
-    static constexpr int NCOL = kAwQBytes / (D * 2);                 // columns of all slots together
+    // streamed queries have the bytes of two K stages more for their slots
+    static constexpr int Q_STREAM = kAwQBytes + (kAwKStages - 2) * K_BYTES;
+    static constexpr int NCOL = Q_STREAM / (D * 2);                  // columns of all slots together
     static constexpr int OFF_SUM = OFF_COL + NCOL * 8;               // [2][3][128] sums of the other warpgroups
     static constexpr int OFF_NV = OFF_SUM + 2 * (kAwWgs - 1) * kAwBM * 4;
              // [kAwCounted] visible entries
@@ -194,18 +204,20 @@ __device__ __forceinline__ void aw_buffer(const WeightParams &p, uint32_t nt, in
     }
 }
 
-template <int D>
+template <int D, bool STREAM>
 __global__ void __launch_bounds__(kAwThreads, 1)
 attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const WeightParams p)
 {
     using SM = WeightSmem<D>;
     constexpr int NCB = D / 64;
+    constexpr int KS_LOG2 = STREAM ? 1 : 2;      // K stages
+    constexpr uint32_t nks = 1u << KS_LOG2;
     extern __shared__ __align__(1024) uint8_t aw_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(aw_smem_raw) + 1023) &
                                                 ~(uintptr_t)1023);
     uint8_t *sQ = smem + SM::OFF_Q;
-    uint8_t *sK = smem + SM::OFF_K;
+    uint8_t *sK = smem + SM::OFF_K + (kAwKStages - nks) * SM::K_BYTES;
     float *sLse = reinterpret_cast<float *>(smem + SM::OFF_COL);       // -lse, log2 units, per slot and column
     int *sNv = reinterpret_cast<int *>(smem + SM::OFF_COL + SM::NCOL * 4);
     float *sSum = reinterpret_cast<float *>(smem + SM::OFF_SUM);
@@ -220,7 +232,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kAwQStages; ++s) {
-            mbar_init(&bar[WB_QF + s], 1 + 32);    // the TMA copy, the lanes of warp 18 or 19
+            mbar_init(&bar[WB_QF + s], 1 + 32);    // the TMA copy, the lanes of the slot's column warp
             mbar_init(&bar[WB_QE + s], 1 + 4 * kAwWgs);   // the MMA, the epilogue warps
         }
         for (int s = 0; s < kAwKStages; ++s) {
@@ -306,19 +318,25 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     f(i, h, tt * p.tpt, ht * p.hpt, tt + ht == 0, tt == p.ntt - 1 && ht == p.nht - 1);
     };
 
-    if (warp == 16 || warp == 18 || warp == 19) {
-        // ============ query blocks: copies (warp 16), lse and counts (warps 18, 19); K tiles (warp 16) ============
+    if (warp >= 16)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAwOtherRegs));
+    // Without a selection two of the gather's warps write columns too.  A slot always has
+    // the same warp: one that ran a fill ahead would take the parity of the fill before
+    // for its own.
+    const int ncw = p.idx ? 2 : 4;
+    if (warp == 16 || (warp >= 18 && warp < 18 + ncw)) {
+        // ============ query blocks: copies (warp 16), lse and counts (warps 18 on); K tiles (warp 16) ============
         uint32_t kc = 0, qc = 0;
         const uint32_t box_bytes = (uint32_t)p.hpt * p.tpt * D * 2;
         while (ok && walk.next(p, lane, r)) {
             for (int tile = r.lo; ok && tile < r.hi; ++tile) {
-                const bool load_q = !p.resident || tile == r.lo;
+                const bool load_q = STREAM || tile == r.lo;
                 if (!load_q && (warp >= 18 || p.idx))
                     break;
                 for_blocks([&](int i, int h, int t0, int h0, bool first, bool) {
                     if (warp == 16 && first && !p.idx) {
-                        const uint32_t st = kc % kAwKStages;
-                        if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
+                        const uint32_t st = kc & (nks - 1);
+                        if (kc >= nks && !(ok = wait(WB_KE + st, ((kc >> KS_LOG2) - 1) & 1)))
                             return;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&bar[WB_KF + st], SM::K_BYTES);
@@ -331,10 +349,10 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                     if (!load_q)
                         return;
-                    const uint32_t st = p.resident ? i : ring, par = p.resident ? runs & 1 : ring_par;
-                    const bool used = p.resident ? runs > 0 : qc >= (uint32_t)p.nqs;
-                    if (warp >= 18 && (st & 1) != (uint32_t)(warp - 18)) {
-                        ++qc;              // the other warp's slot
+                    const uint32_t st = STREAM ? ring : i, par = STREAM ? ring_par : runs & 1;
+                    const bool used = STREAM ? qc >= (uint32_t)p.nqs : runs > 0;
+                    if (warp >= 18 && (st & (ncw - 1)) != (uint32_t)(warp - 18)) {
+                        ++qc;              // another warp's slot
                         advance();
                         return;
                     }
@@ -390,9 +408,9 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         if (warp == 16 && lane == 0) {
             // unwinding: wait for the last copies issued into every slot
-            for (uint32_t c = (kc > kAwKStages ? kc - kAwKStages : 0); c < kc; ++c)
-                drain_wait(&bar[WB_KF + c % kAwKStages], (c / kAwKStages) & 1);
-            if (!p.resident) {
+            for (uint32_t c = (kc > nks ? kc - nks : 0); c < kc; ++c)
+                drain_wait(&bar[WB_KF + (c & (nks - 1))], (c >> KS_LOG2) & 1);
+            if (STREAM) {
                 for (uint32_t c = (qc > (uint32_t)p.nqs ? qc - p.nqs : 0); c < qc; ++c)
                     drain_wait(&bar[WB_QF + c % p.nqs], (c / p.nqs) & 1);
             } else {
@@ -427,8 +445,8 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     if (bad && c8 == 0)
                         set_error(HYB_ERR_DEVICE_BOUNDS);
                     for (int h = 0; h < p.Hkv; ++h) {
-                        const uint32_t st = kc % kAwKStages;
-                        if (kc >= kAwKStages && !(ok = wait(WB_KE + st, ((kc / kAwKStages) - 1) & 1)))
+                        const uint32_t st = kc & (nks - 1);
+                        if (kc >= nks && !(ok = wait(WB_KE + st, ((kc >> KS_LOG2) - 1) & 1)))
                             break;
                         const uint32_t dst = smem_u32(sK + st * SM::K_BYTES) + dchunk;
 #pragma unroll
@@ -453,15 +471,15 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         while (ok && walk.next(p, lane, r)) {
             for (int tile = r.lo; ok && tile < r.hi; ++tile, ++nt) {
                 for_blocks([&](int i, int, int, int, bool first, bool last) {
-                    const uint32_t qs = p.resident ? i : ring, par = p.resident ? runs & 1 : ring_par;
-                    const uint32_t ks = kc % kAwKStages;
+                    const uint32_t qs = STREAM ? ring : i, par = STREAM ? ring_par : runs & 1;
+                    const uint32_t ks = kc & (nks - 1);
                     uint32_t buf, round;
                     aw_buffer(p, nt, nblocks, i, buf, round);
                     if (!(ok = wait(WB_QF + qs, par)))
                         return;
                     advance();
                     if (first) {
-                        if (!(ok = wait(WB_KF + ks, (kc / kAwKStages) & 1)))
+                        if (!(ok = wait(WB_KF + ks, (kc >> KS_LOG2) & 1)))
                             return;
                         if (p.idx)
                             fence_proxy_async_smem();   // rows written by cp.async, read by the MMA
@@ -480,7 +498,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         mma_commit(&bar[WB_SF + buf]);
                         if (last)
                             mma_commit(&bar[WB_KE + ks]);
-                        if (!p.resident || tile == r.hi - 1)
+                        if (STREAM || tile == r.hi - 1)
                             mma_commit(&bar[WB_QE + qs]);
                     }
                     __syncwarp();
@@ -495,6 +513,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         __syncwarp();
         drain_wait(&bar[WB_DONE], 0);
     } else if (warp < 4 * kAwWgs) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAwEpiRegs));
         // ============================ exponentials and sums ============================
         const int x = warp >> 2;
         const int quad = warp & 3;
@@ -518,12 +537,13 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (!p.split && (int)(nt % kAwWgs) != x)
                     continue;                            // another warpgroup's
                 const int j = tile * kAwBM + key;        // entry, or slot of the selection
+                const int key_at = p.idx ? 0 : j;        // every listed entry is seen
                 int e = -1;
                 if (p.idx && (!p.split || x == 0) && j < p.K)
                     e = __ldg(p.idx + (size_t)r.b * p.K + j);
                 float tot = 0.f;
                 for_blocks([&](int i, int, int t0, int h0, bool, bool) {
-                    const uint32_t qs = p.resident ? i : ring, par = p.resident ? runs & 1 : ring_par;
+                    const uint32_t qs = STREAM ? ring : i, par = STREAM ? ring_par : runs & 1;
                     uint32_t buf, round;
                     aw_buffer(p, nt, nblocks, i, buf, round);
                     if (!(ok = wait(WB_QF + qs, par) && wait(WB_SF + buf, round & 1)))
@@ -538,10 +558,10 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const int *cn = sNv + qs * p.NB;
 #pragma unroll 1
                     for (int c = p.split ? 32 * x : 0; c < ncv; c += p.split ? 32 * kAwWgs : 32) {
-                        float sv[32];
-                        tmem_ld32(tS + c, sv);
-                        tmem_ld_wait();
                         if (full && c + 32 <= ncv) {
+                            float sv[32];
+                            tmem_ld32(tS + c, sv);
+                            tmem_ld_wait();
                             uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
                             for (int q = 0; q < 32; q += 4) {
@@ -556,23 +576,34 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                             f2_split(add_f2(s2[0], s2[1]), a0, a1);
                             tot += a0 + a1;
                         } else {
-                            // some columns are padding, or do not see every key of the tile
-                            float s = 0.f;
+                            // some columns are padding (count 0; from NB on there are none), or do
+                            // not see every key of the tile
+#pragma unroll 1
+                            for (int c1 = c; c1 < min(c + 32, ncv); c1 += 16) {
+                                float sv[16], s = 0.f;
+                                tmem_ld16(tS + c1, sv);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int q = 0; q < 32; ++q) {
-                                const int cc = min(c + q, p.NB - 1);
-                                const bool in = c + q < ncv && (p.idx || j < cn[cc]);
-                                const float e = ex2_approx(fmaf(sv[q], p.scale_log2, nl[cc]));
-                                s += in ? e : 0.f;
+                                for (int q = 0; q < 16; q += 4) {
+                                    const float4 l4 = *reinterpret_cast<const float4 *>(nl + c1 + q);
+                                    const int4 n4 = *reinterpret_cast<const int4 *>(cn + c1 + q);
+                                    const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+                                    const int nv[4] = {n4.x, n4.y, n4.z, n4.w};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const float e = ex2_approx(fmaf(sv[q + k], p.scale_log2, l[k]));
+                                        s += key_at < nv[k] ? e : 0.f;
+                                    }
+                                }
+                                tot += s;
                             }
-                            tot += s;
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&bar[WB_SE + buf]);
-                        if (!p.resident)
+                        if (STREAM)
                             mbar_arrive(&bar[WB_QE + qs]);   // this warp has read the slot's columns
                     }
                 });
@@ -609,7 +640,7 @@ attn_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     *a = p.accumulate ? *a + tot : tot;
                 }
             }
-            if (ok && p.resident && r.hi > r.lo) {
+            if (ok && !STREAM && r.hi > r.lo) {
                 // this warp has read the run's columns (it waits for them even where it
                 // had no tile of the run, so that it never releases a slot a run ahead)
                 for (int i = 0; ok && i < nblocks; ++i) {
@@ -644,18 +675,21 @@ static cudaError_t launch_weights_t(WeightParams &p, const void *q, const void *
                                     int num_sms)
 {
     using SM = WeightSmem<D>;
-    p.nqs = kAwQBytes / (p.NB * D * 2);
-    if (p.nqs > kAwQStages)
-        p.nqs = kAwQStages;
+    const int slot = p.NB * D * 2;
+    p.nqs = min(kAwQBytes / slot, kAwQStages);
     p.resident = (long long)p.Hkv * p.ntt * p.nht <= p.nqs;
+    if (!p.resident)
+        p.nqs = min(SM::Q_STREAM / slot, kAwQStages);
     p.split = !p.resident || (long long)p.B * p.tiles < 2LL * num_sms;
     CUtensorMap mq, mk;
     if (!make_map(&mq, q, D, p.Hq, p.Lq, p.B, p.hpt, p.tpt) ||
         !make_map(&mk, kc, D, p.Hkv, p.Nc, p.B, 1, kAwBM))
         return cudaErrorInvalidValue;
     const size_t ask = 1024 + SM::BYTES < 120 * 1024 ? 120 * 1024 : 1024 + SM::BYTES;
-    auto kern = attn_weights_kernel<D>;
+    auto kern = p.resident ? attn_weights_kernel<D, false> : attn_weights_kernel<D, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
+    if (e == cudaSuccess)
+        e = check_reg_split(kern, kAwThreads, 128 * kAwWgs, kAwEpiRegs, kAwOtherRegs);
     if (e != cudaSuccess)
         return e;
     if (p.idx && !p.accumulate) {

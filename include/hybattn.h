@@ -264,7 +264,8 @@ hyb_status hyb_prefix_attn_fwd(const hyb_problem *p, int Np, const void *q, cons
  *   accumulate == 0: acc[b, j] = w[b, j] for every j < Nc (0 where unseen).
  * fp32 sums in a fixed order.  q: [B, Lq, Hq, d], kc: [B, Nc, Hkv, d] bf16,
  * 16-byte aligned; lse: [B, Hq, Lq]; idx: [B, Lq, topk] int32 or NULL (then
- * topk <= 0), with Lq == 1 (else HYB_ERR_UNSUPPORTED; an entry listed twice
+ * topk <= 0), with Lq == 1, topk <= 2048 and at most 64 query heads per KV
+ * head (else HYB_ERR_UNSUPPORTED; an entry listed twice
  * counts twice; entries >= Nc are skipped and flagged as
  * HYB_ERR_DEVICE_BOUNDS); acc: [B, Nc] fp32.  Unseen rows of kc may hold
  * anything. */

@@ -78,6 +78,9 @@ SHAPES = [
     (3, 1, 64, 1, 128, 4, 128, 900, 256),    # a selection
     (2, 1, 8, 2, 64, 4, 128, 500, 77),       # ... of an odd size, two KV heads
     (2, 1, 4, 1, 128, 4, 128, 64, 1),        # ... of one
+    (2, 1, 384, 6, 128, 4, 128, 600, 200),   # ... with more query rows than stay resident
+    (2, 14, 48, 1, 128, 4, 128, 300, 0),     # five slots of 96 rows for seven blocks
+    (2, 40, 64, 2, 64, 3, 9, 400, 0),        # d = 64, streamed
 ]
 
 

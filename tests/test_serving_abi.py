@@ -113,6 +113,7 @@ def _weights(hb, e0=0, swap=None, idx=False, **kw):
     (dict(swap=("lse", 4096 + 2)), "INVALID_ARG"), (dict(swap=("acc", 4096 + 1)), "INVALID_ARG"),
     (dict(idx=True, swap=("idx", 4096 + 2)), "INVALID_ARG"),
     (dict(idx=True, Lq=2), "UNSUPPORTED"), (dict(idx=True, topk=2049), "UNSUPPORTED"), (dict(d=32), "UNSUPPORTED"),
+    (dict(idx=True, B=2, Hq=320, Hkv=1, d=128, Nc=600, topk=200), "UNSUPPORTED"),
     (dict(e0=1 << 30), "UNSUPPORTED"), (dict(B=1 << 20, Lq=1 << 12), "UNSUPPORTED"),
 ])
 def test_weights_refusals(hb, change, status):
