@@ -41,6 +41,8 @@
 // 20-23 gather the selected rows with cp.async when idx is given (16 lanes per row).
 #include "common.cuh"
 
+#include <atomic>
+
 namespace hyb {
 
 constexpr int kAwThreads = 768;
@@ -670,6 +672,9 @@ __global__ void __launch_bounds__(256) attn_weights_zero_kernel(float *acc, long
         acc[i] = 0.f;
 }
 
+// Devices (below 64) on which a kernel's attributes are set, by d and by layout.
+static std::atomic<unsigned long long> g_weights_ready[2][2];
+
 template <int D>
 static cudaError_t launch_weights_t(WeightParams &p, const void *q, const void *kc, cudaStream_t stream,
                                     int num_sms)
@@ -687,11 +692,20 @@ static cudaError_t launch_weights_t(WeightParams &p, const void *q, const void *
         return cudaErrorInvalidValue;
     const size_t ask = 1024 + SM::BYTES < 120 * 1024 ? 120 * 1024 : 1024 + SM::BYTES;
     auto kern = p.resident ? attn_weights_kernel<D, false> : attn_weights_kernel<D, true>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
-    if (e == cudaSuccess)
-        e = check_reg_split(kern, kAwThreads, 128 * kAwWgs, kAwEpiRegs, kAwOtherRegs);
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    std::atomic<unsigned long long> &ready = g_weights_ready[D == 128][!p.resident];
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ask);
+        if (e == cudaSuccess)
+            e = check_reg_split(kern, kAwThreads, 128 * kAwWgs, kAwEpiRegs, kAwOtherRegs);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
     if (p.idx && !p.accumulate) {
         const long long n = (long long)p.B * p.Nc;
         const long long blocks = (n + 1023) / 1024;
