@@ -655,7 +655,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         uint8_t *stage = smem + SM::OFF_ST + warp * SM::STAGE_BYTES;
         const int rtok = row / p.hpt, rhead = row % p.hpt;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        uint32_t scnt = 0, ocnt = 0, nq = 0;
+        uint32_t scnt = 0, nq = 0;
+        uint32_t o_par = 0;                 // bit y: parity of the next phase of stream y's O
         uint32_t theirs = 0;                // tiles of the other warpgroups so far
         bool ok = true;
         PrefixItem it;
@@ -793,13 +794,20 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             }
             if (!ok)
                 break;
-            // epilogue: this item's part of the row
-            if (first < it.nt) {
-                if (!(ok = wait(PB_OF + x, ocnt & 1)))
-                    break;
-                ++ocnt;
-                tc_fence_after();
+            // Epilogue: the O's that this warp frees, its own or (joint) both streams'.  A
+            // warp without rows waits too: freeing takes no look at O, and one that ran
+            // items ahead would stand in for a warp that still reads this item's.  So an O's
+            // next phase needs this item freed by all sixteen warps.
+            const bool joint = p.direct && !it.pair;
+            const int o_end = joint ? min(it.nt, 2) : first < it.nt ? x + 1 : x;
+#pragma unroll 1
+            for (int y = joint ? 0 : x; ok && y < o_end; ++y) {
+                ok = wait(PB_OF + y, (o_par >> y) & 1);
+                o_par ^= 1u << y;
             }
+            if (!ok)
+                break;
+            tc_fence_after();
             if (!p.direct) {
                 // a part of the row: this warpgroup's O as it is, its maximum and sum
                 if (warp_rows) {
@@ -875,7 +883,6 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             // The row's sum over both halves, and where an alternating item is joined the two
             // streams' maxima and sums: weights ws of this warpgroup's (pair) or of A's
             // and B's O, maximum m_ref and sum l_sum of the result.
-            const bool joint = !it.pair;
             float ws[2] = {1.f, 0.f};
             if (warp_rows) {
                 float2 *ml = reinterpret_cast<float2 *>(stage) + lane;
@@ -895,7 +902,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                         mbar_arrive(&bar[PB_MEET4 + quad]);
                     if (!(ok = wait(PB_MEET4 + quad, met4++ & 1)))
                         break;
-                    tc_fence_after();          // the other warpgroup's O, which it waited for
+                    tc_fence_after();
                     const float l0 = l_sum + of->y, l1 = ml[hop].y + of[hop].y, m1 = ml[hop].x;
                     const float M = fmaxf(m_ref, m1);
                     const float w0 = l0 != 0.f ? exp2f(m_ref - M) : 0.f, w1 = l1 != 0.f ? exp2f(m1 - M) : 0.f;
