@@ -230,7 +230,7 @@ static_assert(1024 + PrefixSmem<128>::BYTES <= 227 * 1024, "shared memory of a C
 
 // barrier slots (two each from PB_KF on, three item slots)
 enum { PB_QF = 0, PB_QE = 1, PB_KF = 2, PB_KE = 4, PB_VF = 6, PB_VE = 8, PB_SF = 10, PB_PF = 12, PB_OF = 14,
-       PB_OE = 16, PB_IF = 18, PB_IE = 21, PB_DONE = 24, PB_MEET = 25, PB_MEET4 = 33 };
+       PB_OE = 16, PB_IF = 18, PB_IE = 21, PB_DONE = 24, PB_MEET = 25, PB_MEET4 = 33, PB_TURN = 37 };
 
 // Entries visible to position pos: those ending before its window.
 __device__ __forceinline__ int pf_visible(long long pos, int m, int W, int n)
@@ -387,6 +387,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
             mbar_init(&bar[PB_VE + s], 2);
             mbar_init(&bar[PB_SF + s], 1);
             mbar_init(&bar[PB_PF + s], 8);     // one arrival a warp
+            mbar_init(&bar[PB_TURN + s], 8);
             mbar_init(&bar[PB_OF + s], 1);
             mbar_init(&bar[PB_OE + s], 16);    // both warpgroups (joint), or two from one
         }
@@ -657,7 +658,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
         uint32_t scnt = 0, nq = 0;
         uint32_t o_par = 0;                 // bit y: parity of the next phase of stream y's O
-        uint32_t theirs = 0;                // tiles of the other warpgroups so far
+        uint32_t turn = 0;                  // tiles taken in turns so far
         bool ok = true;
         PrefixItem it;
         while (ok && item(nq, it)) {
@@ -749,8 +750,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                     // Turns: B's exponentials of a tile follow A's, and A's next ones follow
                     // B's, so that one query tile's run under the other's MMAs.  (Left
                     // alone the two fall into step: both exponentiate, then both wait.)
-                    if (turns && (x || t > 0) &&
-                        !(ok = wait(PB_PF + (x ^ 1), (x ? theirs + t : theirs + t - 1) & 1)))
+                    // Turns have barriers of their own and are counted over all items (those
+                    // between may take none): A's turn n + 1 ends only once every A warp with
+                    // rows has seen the end of B's turn n, and B's turn n only once every B
+                    // warp with rows has seen the end of A's, so that neither barrier gets
+                    // two phases ahead of a warp that waits by parity.
+                    if (turns && (x || turn > 0) && !(ok = wait(PB_TURN + (x ^ 1), (x ? turn : turn - 1) & 1)))
                         break;
                     // P = exp2(s * scale - mu), rounded to bf16 (the MMA operand; its
                     // relative error 2^-8 a term averages out below the output's own
@@ -789,8 +794,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
+                    if (turns)                 // before P: the next tile's S follows it
+                        mbar_arrive(&bar[PB_TURN + x]);
                     mbar_arrive(&bar[PB_PF + x]);
+                }
+                turn += turns;
             }
             if (!ok)
                 break;
@@ -876,7 +885,6 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                     mbar_arrive(&bar[PB_OE + x]);
                     mbar_arrive(&bar[PB_OE + x]);
                 }
-                theirs += turns ? it.nt : it.pair ? (x ? it.nt : 0) : (it.nt + x) / 2;
                 ++nq;
                 continue;
             }
@@ -1009,7 +1017,6 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_const
                         mbar_arrive(&bar[PB_OE + 1]);
                 }
             }
-            theirs += turns ? it.nt : it.pair ? (x ? it.nt : 0) : (it.nt + x) / 2;
             ++nq;
         }
     }

@@ -38,3 +38,17 @@ def _check_case(hb, B, Lq, Hq, Hkv, d, m, W, Np, Nc, repeats=10):
 ])
 def test_single_query_tiles(hb, B, Lq, Hq, Hkv, d, m, W, Np, Nc):
     _check_case(hb, B, Lq, Hq, Hkv, d, m, W, Np, Nc)
+
+
+# Two query tiles an item, whose exponentials go in turns: several such items a CTA,
+# beside items of one query tile and items whose key tiles alternate.  The turns of one
+# item follow those of the item before it.
+@pytest.mark.parametrize("B,Lq,Hq,Hkv,d,m,W,Np,Nc", [
+    (40, 130, 8, 8, 64, 4, 16, 30, 200),     # three a CTA, o written by the items themselves
+    (16, 260, 8, 8, 64, 4, 16, 100, 150),    # a pair, then the sequence's third query tile alone
+    (12, 70, 80, 16, 128, 4, 30, 260, 200),  # five heads a tile, three tiles a sequence
+    (100, 1, 512, 16, 64, 4, 0, 1000, 150),  # up to two over the shared entries, then alternating items
+    (64, 1, 256, 16, 128, 4, 128, 2000, 300),
+])
+def test_query_tiles_in_turns(hb, B, Lq, Hq, Hkv, d, m, W, Np, Nc):
+    _check_case(hb, B, Lq, Hq, Hkv, d, m, W, Np, Nc)
