@@ -437,10 +437,14 @@ class _On:
         self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
     def new(self, shape, dtype):
-        """A tensor for this call; the allocator keeps it until the stream is done with it."""
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.stream is not None:
-            t.record_stream(self.stream)
+        """A tensor for this call, from the memory pool of the call's stream: a block that
+        was freed on the caller's stream may still be in use there.  The allocator keeps
+        it until both streams are done with it."""
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def __enter__(self):
