@@ -158,8 +158,10 @@ struct PrefixParams {
 // 2^x for a pair without the exponential unit: x = i + f with i the nearest
 // integer (read off the low bits of x + 1.5 2^23), 2^f by its degree-4 minimax
 // polynomial on [-1/2, 1/2] (fitted by iteratively reweighted least squares;
-// relative error below 2.8e-6, far inside the rounding of P to bf16), i added to the exponent
-// field.  Below -126 (masked scores are -infinity) the result is 0; x <= 8 here.
+// relative error below 2.8e-6, far inside the rounding of P to bf16), times 2^i from i in
+// the exponent field.  Below -126 (masked scores are -infinity) the result is 0; x <= 8
+// here.  A NaN stays one, through the product (added to the exponent field, i would
+// turn NaN's bits into those of a large number).
 __device__ __forceinline__ void exp2_poly2(float x0, float x1, float &e0, float &e1)
 {
     const uint64_t x = f2(x0, x1);
@@ -170,11 +172,12 @@ __device__ __forceinline__ void exp2_poly2(float x0, float x1, float &e0, float 
     q = fma_f2(q, f, f2(0.24024744f, 0.24024744f));
     q = fma_f2(q, f, f2(0.69312179f, 0.69312179f));
     q = fma_f2(q, f, f2(0.99999928f, 0.99999928f));
-    float t0, t1, q0, q1;
+    float t0, t1;
     f2_split(t, t0, t1);
-    f2_split(q, q0, q1);
-    e0 = x0 < -126.f ? 0.f : __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
-    e1 = x1 < -126.f ? 0.f : __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+    f2_split(mul_f2(q, f2(__uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u),
+                          __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u))), e0, e1);
+    e0 = x0 < -126.f ? 0.f : e0;
+    e1 = x1 < -126.f ? 0.f : e1;
 }
 
 // A work item, as the roles read it from shared memory.

@@ -579,6 +579,13 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b)
     return d;
 }
 
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a run of
 // 128-byte-swizzled rows (the layout TMA writes with SWIZZLE_128B).
 __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t chunk)

@@ -242,7 +242,8 @@ hyb_status hyb_gated_fwd(const hyb_problem *p, const void *q, const void *kc, co
  * (own) sees may hold anything, NaN included; so may raw rows outside a
  * sequence's windows (from its lowest to its highest query position).  What some
  * query of the call sees has to be finite: a NaN or an infinity in its value row
- * may also reach queries that do not see it (a weight of 0 times NaN).
+ * may also reach queries that do not see it (a weight of 0 times NaN).  A score
+ * that is NaN or +infinity makes the lse of its row NaN.
  * ws: hyb_prefix_workspace_size(p, Np) bytes, 256-byte aligned (0 bytes: NULL
  * will do); calls that may run at the same time need a workspace each. */
 size_t hyb_prefix_workspace_size(const hyb_problem *p, int Np);
