@@ -156,22 +156,24 @@ struct PrefixParams {
 };
 
 // 2^x for a pair without the exponential unit: x = i + f with i the nearest
-// integer (read off the low bits of x + 1.5 2^23), 2^f by its degree-4 minimax
-// polynomial on [-1/2, 1/2] (fitted by iteratively reweighted least squares;
-// relative error below 2.8e-6, far inside the rounding of P to bf16), times 2^i from i in
-// the exponent field.  Below -126 (masked scores are -infinity) the result is 0; x <= 8
-// here.  A NaN stays one, through the product (added to the exponent field, i would
-// turn NaN's bits into those of a large number).
+// integer (read off the low bits of x + 1.5 2^23), 2^f by its degree-5 minimax
+// polynomial on [-1/2, 1/2] with 2^0 = 1 (fitted by iteratively reweighted least
+// squares; 1.7e-7 off at most in fp32, relative, where the unit is 2^-22: lse is as good as
+// with the unit alone), times 2^i from i in the exponent field.  Below -126 (masked
+// scores are -infinity) the result is 0; x <= 8 here.  A NaN stays one, through the
+// product (added to the exponent field, i would turn NaN's bits into those of a large
+// number).
 __device__ __forceinline__ void exp2_poly2(float x0, float x1, float &e0, float &e1)
 {
     const uint64_t x = f2(x0, x1);
     const uint64_t t = add_f2(x, f2(12582912.f, 12582912.f));
     const uint64_t i = add_f2(t, f2(-12582912.f, -12582912.f));
     const uint64_t f = fma_f2(i, f2(-1.f, -1.f), x);
-    uint64_t q = fma_f2(f, f2(0.0095701003f, 0.0095701003f), f2(0.055917859f, 0.055917859f));
-    q = fma_f2(q, f, f2(0.24024744f, 0.24024744f));
-    q = fma_f2(q, f, f2(0.69312179f, 0.69312179f));
-    q = fma_f2(q, f, f2(0.99999928f, 0.99999928f));
+    uint64_t q = fma_f2(f, f2(0.00132647273f, 0.00132647273f), f2(0.00967151299f, 0.00967151299f));
+    q = fma_f2(q, f, f2(0.0555073358f, 0.0555073358f));
+    q = fma_f2(q, f, f2(0.240222424f, 0.240222424f));
+    q = fma_f2(q, f, f2(0.693147004f, 0.693147004f));
+    q = fma_f2(q, f, f2(1.f, 1.f));
     float t0, t1;
     f2_split(t, t0, t1);
     f2_split(mul_f2(q, f2(__uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u),

@@ -1,5 +1,7 @@
-"""The exponentials of hyb_prefix_attn_fwd, seen through the fp32 lse: values that
-are not finite, at every place of a key among its tile's."""
+"""The exponentials of hyb_prefix_attn_fwd, seen through the fp32 lse: their error
+where few keys with small scores leave nothing else, and values that are not
+finite, at every place of a key among its tile's."""
+import numpy as np
 import pytest
 import torch
 
@@ -39,3 +41,29 @@ def test_a_score_that_is_not_finite_shows_in_lse(hb, B, Hq, part):
                 hb.hyb_prefix_attn_fwd(p, q, None, None, None, None, each(k), each(v), lse=lse)
             assert torch.all(torch.isnan(lse)), (bad, at)
     assert hb.hyb_get_device_status() == hb.HYB_OK
+
+
+@pytest.mark.parametrize("Hq", [100, 176])              # one query tile; two
+@pytest.mark.parametrize("n", [4, 16, 77])
+def test_exponentials_are_as_good_as_the_hardwares(hb, Hq, n):
+    # key 0 has score 0 and all others -s_h, exact in fp32: lse = log(1 + (n - 1) exp(-s_h)).
+    # Error of a weight w = 2^-x, x = s log2(e): 2^-22 for 2^x, and x rounds twice (log2(e)
+    # and the product), 2^-24 x each, which moves w by ln 2 as much; n fp32 terms, 2^-24 of
+    # the sum each; log2 to 2^-23 of itself or of 1 (its units in the last place), and
+    # twice 2^-24 for its product with ln 2.
+    d = 64
+    q = torch.zeros((1, 1, Hq, d))
+    q[0, 0, :, 7] = torch.arange(Hq) / 16                # bf16 holds these
+    k = torch.zeros((n, 1, d))
+    k[1:, 0, 7] = -1
+    q_pos = torch.full((1, 1), n - 1, dtype=torch.int32, device="cuda")
+    p = hb.problem(B=1, Lq=1, Lkv=0, Hq=Hq, Hkv=1, d=d, m=1, W=0, Nc=0, q_pos=q_pos)
+    lse = torch.zeros((1, Hq, 1), device="cuda")
+    hb.hyb_prefix_attn_fwd(p, q.bfloat16().cuda(), k.bfloat16().cuda(), torch.zeros_like(k).bfloat16().cuda(), lse=lse)
+    s = np.arange(Hq) / 16 / 8                           # the scale is 1 / sqrt(64)
+    w = (n - 1) * np.exp(-s)
+    want, share, x = np.log1p(w), w / (1 + w), s / np.log(2)
+    tol = share * (2.0 ** -22 + np.log(2) * 2 * 2.0 ** -24 * x) + n * 2.0 ** -24
+    tol += np.log(2) * 2.0 ** -23 * np.maximum(want / np.log(2), 1) + 2 * 2.0 ** -24 * want
+    err = np.abs(lse[0, :, 0].double().cpu().numpy() - want)
+    assert np.all(err <= tol), float((err / tol).max())
