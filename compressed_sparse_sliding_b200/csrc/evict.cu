@@ -6,7 +6,8 @@
 // interval over at most three 2048-bin histograms (the interval starts at the
 // candidates' own minimum and maximum, so that the bins spread the values that
 // occur), then the chosen entries are emitted in index order, lower index first
-// among equal weights.  One cluster of up to 16 CTAs per sequence; each CTA's
+// among equal weights.  One cluster of up to 16 CTAs per sequence (8 where the device,
+// or the part of it that the process has, cannot place sixteen); each CTA's
 // slice lives in registers, K entries a thread, read once, coalesced.  Over
 // distributed shared memory go only the non-empty bins, to the first CTA, which
 // finds the threshold's bin and, as soon as that holds at most 2048 keys, collects
@@ -15,7 +16,8 @@
 // Emission is by ballots: word w of the slice's bit map is 32 entries, one block
 // scan over the words' counts places them all.  Bound: latency (4 bytes read per
 // entry; two cluster barriers a histogram).
-// evict_select_long_kernel takes sequences of more than 16 x 32768 entries: a
+// evict_select_long_kernel takes sequences of more entries than that cluster's threads
+// hold (16 x 32768): a
 // radix search with slices that are read again from L2 in each pass.
 //
 // cache_compact_kernel.  out[b, i] = cache[b, keep[b, i]], a gather of whole
@@ -23,14 +25,14 @@
 // kept bytes.  A block copies a run of rows of one cache; a row's threads hold
 // 16-byte pieces of four rows each, all loads before the first store.  (256-byte
 // rows, half of 16384 kept: 6.0 TB/s, as cudaMemcpy moves the same bytes.)
+#include <atomic>
+
 #include "common.cuh"
+#include "evict_plan.cuh"
 
 namespace hyb {
 
-constexpr int kEvThreads = 1024;
 constexpr int kEvBins = 2048;
-constexpr int kEvCluster = 16;          // CTAs of a sequence at most (over 8: opted in)
-constexpr int kEvKeysMax = 32;          // keys per thread held in registers
 constexpr int kEvList = 2 * kEvThreads; // keys that the first CTA finishes alone
 
 // Larger weight, larger key; -0 equals +0, NaN ranks as -infinity.
@@ -530,17 +532,77 @@ __global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(const Evict
     }
 }
 
-template <int K>
-static cudaError_t launch_evict_t(const EvictParams &p, cudaLaunchConfig_t &cfg)
+// The kernel that holds K keys per thread (0: the long one).
+typedef void (*EvictKernel)(EvictParams);
+static EvictKernel evict_kernel(int keys)
 {
-    auto kern = evict_select_kernel<K>;
+    switch (keys) {
+    case 0: return evict_select_long_kernel;
+    case 1: return evict_select_kernel<1>;
+    case 2: return evict_select_kernel<2>;
+    case 4: return evict_select_kernel<4>;
+    case 8: return evict_select_kernel<8>;
+    case 16: return evict_select_kernel<16>;
+    default: return evict_select_kernel<32>;
+    }
+}
+
+static void evict_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[2], int ranks, int B, cudaStream_t stream)
+{
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)ranks;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg = {};
+    cfg.gridDim = dim3((unsigned)ranks, (unsigned)B);
+    cfg.blockDim = dim3(kEvThreads);
     cfg.dynamicSmemBytes = sizeof(EvictShared);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(EvictShared));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+}
+
+// The largest cluster that the current device can place, after setting the kernels'
+// attributes; asked once per device (below 64), like the attributes.
+static std::atomic<int> g_evict_cluster[64];
+
+static cudaError_t evict_cluster(int &cluster)
+{
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    const bool known = dev >= 0 && dev < 64;
+    cluster = known ? g_evict_cluster[dev].load(std::memory_order_acquire) : 0;
+    if (cluster)
+        return cudaSuccess;
+    cluster = kEvCluster;
+    for (int keys = 0; keys <= kEvKeysMax; keys = keys ? 2 * keys : 1) {
+        EvictKernel kern = evict_kernel(keys);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(EvictShared));
+        if (e == cudaSuccess && keys)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess)
+            return e;
+        if (!keys)
+            continue;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute at[2];
+        evict_config(cfg, at, kEvCluster, 1, nullptr);
+        cfg.attrs = &at[1];            // the cluster alone
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess || n < 1) {
+            cudaGetLastError();        // (a part of a GPU may refuse the question itself)
+            cluster = kEvPortable;
+        }
+    }
+    if (known)
+        g_evict_cluster[dev].store(cluster, std::memory_order_release);
+    return cudaSuccess;
 }
 
 cudaError_t launch_evict_select(const float *acc, int B, int Nc, const int32_t *n_valid, int n_keep, int n_first,
@@ -554,49 +616,16 @@ cudaError_t launch_evict_select(const float *acc, int B, int Nc, const int32_t *
     p.n_keep = n_keep;
     p.n_first = n_first;
     p.n_last = n_last;
-    // CTAs a sequence: more while SMs are free and a slice keeps two keys a thread,
-    // and as many as let the keys stay in registers
-    int ranks = 1;
-    while (ranks < kEvCluster && (long long)B * ranks * 2 <= num_sms && Nc / (ranks * 2) >= 2 * kEvThreads)
-        ranks *= 2;
-    while (ranks < kEvCluster && Nc > ranks * kEvKeysMax * kEvThreads)
-        ranks *= 2;
-    const int per = (Nc + ranks - 1) / ranks;
-    int K = 1;
-    while (K < kEvKeysMax && K * kEvThreads < per)
-        K *= 2;
-    const bool lng = K * kEvThreads < per;
-    if (lng)
-        ranks = 8;
-    // slices of whole 4-entry groups
-    p.slice = ((Nc + ranks - 1) / ranks + 3) & ~3;
-    cudaLaunchConfig_t cfg = {};
+    int cluster = 0;
+    const cudaError_t e = evict_cluster(cluster);
+    if (e != cudaSuccess)
+        return e;
+    const EvictPlan plan = evict_plan(B, Nc, num_sms, cluster);
+    p.slice = plan.slice;
+    cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)ranks;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)ranks, (unsigned)B);
-    cfg.blockDim = dim3(kEvThreads);
-    cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    if (lng) {
-        cfg.dynamicSmemBytes = sizeof(EvictShared);
-        const cudaError_t e = cudaFuncSetAttribute(evict_select_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)sizeof(EvictShared));
-        return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, evict_select_long_kernel, p);
-    }
-    switch (K) {
-    case 1: return launch_evict_t<1>(p, cfg);
-    case 2: return launch_evict_t<2>(p, cfg);
-    case 4: return launch_evict_t<4>(p, cfg);
-    case 8: return launch_evict_t<8>(p, cfg);
-    case 16: return launch_evict_t<16>(p, cfg);
-    default: return launch_evict_t<32>(p, cfg);
-    }
+    evict_config(cfg, at, plan.ranks, B, stream);
+    return cudaLaunchKernelEx(&cfg, evict_kernel(plan.keys), p);
 }
 
 constexpr int kCpArrays = 7;
