@@ -231,6 +231,12 @@ hyb_status hyb_gated_fwd(const hyb_problem *p, const void *q, const void *kc, co
  *   raw keys  positions max(0, t-W+1) .. t (rows p - kv_pos0[b]),
  * with o, lse, an empty key set and positions as in hyb_attn_fwd.  m = 1, W = 0
  * makes every entry one token: plain attention behind a shared prompt.
+ * Behind a prompt of P tokens that the batch shares (W >= 1): share at most the
+ * (P - W + 1) / m entries that end before the window of the first token to come,
+ * and put the prompt's tokens from Np * m on through hyb_decode_append into every
+ * sequence's own ring and caches (t_new = 0, 1, ...), so that the ring holds the
+ * first window's rows; q_pos is then t_new + Np * m, and kv_pos0 what the append
+ * gave + Np * m.
  * The prefix is read once for the query rows of all sequences together, and
  * long key ranges are split over the GPU and joined from fp32 partial results
  * in ws (the join is in a fixed order: equal calls give equal bits).
@@ -281,12 +287,14 @@ hyb_status hyb_attn_weights(const hyb_problem *p, const void *q, const void *kc,
  * -infinity).  keep[b, :]: their indices, ascending, -1 padded.
  * acc: [B, Nc] fp32; keep: [B, n_keep] int32; n_first + n_last <= n_keep;
  * B <= 65535.
- * Positions after an eviction: the caches of a sequence that lost E entries are
- * those of one that is m * E tokens shorter; take m * E off the positions given
- * to later calls (t_new, q_pos).  hyb_decode_append finds its ring rows by
- * position mod W, so choose n_keep such that m * E is a multiple of W, and
- * n_last >= ceil(W / m) + 1, so that the entries that still overlap the window
- * stay the last ones. */
+ * Positions after an eviction: the caches of a sequence that lost
+ * E = max(n - n_keep, 0) entries are those of one that is m * E tokens shorter;
+ * take m * E off the positions given to later calls (t_new, q_pos).
+ * hyb_decode_append finds its ring rows by position mod W: unless m * E is a
+ * multiple of W, move row r of each ring, in both halves of k_ring and v_ring,
+ * to row (r - m * E) mod W as well (in a ragged batch every sequence has its own
+ * E).  Choose n_last >= ceil(W / m) + 1, so that the entries that still overlap
+ * the window stay the last ones. */
 hyb_status hyb_evict_select(const float *acc, int B, int Nc, const int32_t *n_valid, int n_keep, int n_first,
                             int n_last, int32_t *keep, cudaStream_t stream);
 
