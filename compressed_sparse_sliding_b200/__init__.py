@@ -19,7 +19,7 @@ Entry points (same names as the C ABI):
   hyb_attn_bwd,        gradients for training: through the attention (fixed
   hyb_hca_compress_bwd selection) and through block_merge
   hyb_prefix_attn_fwd  attention for a batch whose sequences share a prefix of
-                       compressed entries, stored and read once
+                       compressed entries, stored once
   hyb_attn_weights     the attention weight each cached entry received
   hyb_evict_select,    eviction from full caches by that weight: the entries to
   hyb_cache_compact*   keep, and the (bf16 or 4-bit) caches rewritten with them

@@ -30,9 +30,9 @@
 //
 // Measured (one B200, both kernels, d = 128): two query tiles take a key tile in
 // about 3900 clocks (1.2 PFLOP/s over the GPU; 2048 of them MMAs); 64 sequences, 64 / 1
-// heads over 16384 shared and 2048 own entries: 62.5 us (0.6 PFLOP/s); 64 / 8 heads over
-// 1024 and 64: 36 us, most of it what an item costs beside its tiles; chunks of 256
-// tokens behind 2048 entries: 64 us.  Short items are bound by instruction fetch (the
+// heads over 16384 shared and 2048 own entries: 62 us (0.6 PFLOP/s); 64 / 8 heads over
+// 1024 and 64: 34 us, most of it what an item costs beside its tiles; chunks of 256
+// tokens behind 2048 entries: 63 us.  Short items are bound by instruction fetch (the
 // SM's instruction cache hits 83 % there, 95 % and more with long streams): keeping the
 // code of the item loop short was worth more than fewer operations in it.
 //

@@ -87,8 +87,7 @@ struct WeightSmem {
     static constexpr int Q_STREAM = kAwQBytes + (kAwKStages - 2) * K_BYTES;
     static constexpr int NCOL = Q_STREAM / (D * 2);                  // columns of all slots together
     static constexpr int OFF_SUM = OFF_COL + NCOL * 8;               // [2][3][128] sums of the other warpgroups
-    static constexpr int OFF_NV = OFF_SUM + 2 * (kAwWgs - 1) * kAwBM * 4;
-             // [kAwCounted] visible entries
+    static constexpr int OFF_NV = OFF_SUM + 2 * (kAwWgs - 1) * kAwBM * 4;   // [kAwCounted] visible entries
     static constexpr int OFF_CUM = OFF_NV + kAwCounted * 4;          // [kAwCounted + 1] visible tiles before
     static constexpr int OFF_BAR = OFF_CUM + (kAwCounted + 4) * 4;
     static constexpr int OFF_MISC = OFF_BAR + 64 * 8;

@@ -237,9 +237,11 @@ hyb_status hyb_gated_fwd(const hyb_problem *p, const void *q, const void *kc, co
  * sequence's own ring and caches (t_new = 0, 1, ...), so that the ring holds the
  * first window's rows; q_pos is then t_new + Np * m, and kv_pos0 what the append
  * gave + Np * m.
- * The prefix is read once for the query rows of all sequences together, and
- * long key ranges are split over the GPU and joined from fp32 partial results
- * in ws (the join is in a fixed order: equal calls give equal bits).
+ * The prefix is read once for the query rows of all sequences together, or,
+ * where the call reckons that faster (short prefixes, many query rows a
+ * sequence), by every sequence on its way to its own entries.  Long key ranges
+ * are split over the GPU and joined from fp32 partial results in ws (the join is
+ * in a fixed order: equal calls give equal bits).
  * p: topk <= 0 (else HYB_ERR_UNSUPPORTED), scale >= 0; Nc, Np and W may be 0,
  * and the pointers of absent parts NULL.  q: [B, Lq, Hq, d]; kp, vp:
  * [Np, Hkv, d]; kc, vc: [B, Nc, Hkv, d]; k_raw, v_raw: [B, Lkv, Hkv, d], all

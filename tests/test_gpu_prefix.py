@@ -114,9 +114,9 @@ def _ref(c, q_pos, kv0, m, W):
     (1, 1, 1, 1, 64, 1, 1, 1, 1),            # one of everything
     (1, 1, 8, 1, 128, 4, 128, 20000, 0),     # a long prefix for one token: many splits
     (4, 3, 32, 1, 128, 4, 128, 900, 700),    # 96 rows a sequence: three lane quadrants
-    (3, 1, 40, 1, 64, 4, 16, 500, 1200),     # 40 rows: two copies, the second partly filled
+    (3, 1, 40, 1, 64, 4, 16, 500, 1200),     # 40 rows: two lane quadrants, one partly filled
     (70, 1, 33, 1, 128, 4, 128, 40, 300),    # 33 rows
-    (60, 1, 8, 1, 128, 4, 0, 0, 513),        # eight rows over own entries: four copies
+    (60, 1, 8, 1, 128, 4, 0, 0, 513),        # eight rows over own entries alone
     (2, 130, 2, 1, 128, 4, 128, 1500, 300),  # a chunk: one stream a sequence, whole
     (1, 300, 8, 8, 64, 4, 30, 5000, 64),     # ... and cut
 ])
