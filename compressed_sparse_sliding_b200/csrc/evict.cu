@@ -595,10 +595,10 @@ static cudaError_t evict_cluster(int &cluster)
         cfg.numAttrs = 1;
         int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-        if (e != cudaSuccess || n < 1) {
+        if (e != cudaSuccess)
             cudaGetLastError();        // (a part of a GPU may refuse the question itself)
+        if (e != cudaSuccess || n < 1)
             cluster = kEvPortable;
-        }
     }
     if (known)
         g_evict_cluster[dev].store(cluster, std::memory_order_release);
